@@ -1350,36 +1350,12 @@ slora_status slora_segments_upload(slora_segments* s, void* dev_meta, size_t dev
   if (dev_meta_bytes < meta_bytes_of(s)) return fail(SLORA_E_NOMEM, "slora_segments_upload: dev_meta smaller than meta_bytes");
   slora_pool* p = s->pool;
   if (bytes > 0) {
-    slora_status st = set_device(p);
-    if (st != SLORA_OK) return st;
-    const int slot = p->meta_slot;
-    hipError_t e = hipSuccess;
-    if (p->meta_done[slot]) {
-      e = hipEventSynchronize(p->meta_done[slot]);  // the slot's previous copy has finished
-      if (e != hipSuccess) return hip_fail(e, "hipEventSynchronize(metadata slot)");
-    } else {
-      e = hipEventCreateWithFlags(&p->meta_done[slot], hipEventDisableTiming);
-      if (e != hipSuccess) { p->meta_done[slot] = nullptr; return hip_fail(e, "hipEventCreate"); }
-    }
-    if (p->h_meta_bytes[slot] < bytes) {
-      if (p->h_meta[slot]) (void)hipHostFree(p->h_meta[slot]);
-      p->h_meta[slot] = nullptr;
-      p->h_meta_bytes[slot] = 0;
-      const size_t want = std::max<size_t>(bytes, 1 << 20);
-      e = hipHostMalloc((void**)&p->h_meta[slot], want, hipHostMallocDefault);
-      if (e != hipSuccess) { p->h_meta[slot] = nullptr; return hip_fail(e, "hipHostMalloc(metadata)"); }
-      p->h_meta_bytes[slot] = want;
-    }
-    std::memcpy(p->h_meta[slot], s->blob.data(), bytes);
     hipStream_t st_ = static_cast<hipStream_t>(stream);
-    e = hipMemcpyAsync(dev_meta, p->h_meta[slot], bytes, hipMemcpyHostToDevice, st_);
-    if (e != hipSuccess) return hip_fail(e, "hipMemcpyAsync(metadata)");
-    e = hipEventRecord(p->meta_done[slot], st_);
-    if (e != hipSuccess) return hip_fail(e, "hipEventRecord(metadata)");
-    p->meta_slot ^= 1;
+    slora_status st = pool_upload(p, dev_meta, s->blob.data(), bytes, st_);
+    if (st != SLORA_OK) return st;
     // error word and v pairs start at zero; fused launches count epochs from 1
-    e = launch_zero_words(static_cast<int32_t*>(dev_meta) + s->error_off_words,
-                          (int64_t)(meta_bytes_of(s) / 4) - s->error_off_words, st_);
+    hipError_t e = launch_zero_words(static_cast<int32_t*>(dev_meta) + s->error_off_words,
+                                     (int64_t)(meta_bytes_of(s) / 4) - s->error_off_words, st_);
     if (e != hipSuccess) return hip_fail(e, "zeroing the fused-launch area");
   }
   s->dev_meta = static_cast<const int32_t*>(dev_meta);
@@ -1415,6 +1391,49 @@ slora_status slora_segments_read_error(const slora_segments* s, void* stream, in
 slora_status slora::pool_device_current(slora_pool* p) {
   if (!p) return fail(SLORA_E_INVAL, "NULL pool");
   return set_device(p);
+}
+
+bool slora::pool_info(const slora_pool* p, PoolInfo* info) {
+  if (!p) return false;
+  info->dtype = p->d.dtype;
+  info->n_classes = p->d.n_classes;
+  for (int c = 0; c < 2; ++c) {
+    const bool has = c < p->d.n_classes;
+    info->page_bytes[c] = has ? p->page_bytes[c] : 0;
+    info->n_pages[c] = has ? p->d.n_pages[c] : 0;
+    info->base[c] = has ? static_cast<char*>(p->d.class_base[c]) : nullptr;
+  }
+  return true;
+}
+
+slora_status slora::pool_upload(slora_pool* p, void* dst, const void* src, size_t bytes, hipStream_t stream) {
+  slora_status st = set_device(p);
+  if (st != SLORA_OK) return st;
+  const int slot = p->meta_slot;
+  hipError_t e = hipSuccess;
+  if (p->meta_done[slot]) {
+    e = hipEventSynchronize(p->meta_done[slot]);  // the slot's previous copy has finished
+    if (e != hipSuccess) return hip_fail(e, "hipEventSynchronize(metadata slot)");
+  } else {
+    e = hipEventCreateWithFlags(&p->meta_done[slot], hipEventDisableTiming);
+    if (e != hipSuccess) { p->meta_done[slot] = nullptr; return hip_fail(e, "hipEventCreate"); }
+  }
+  if (p->h_meta_bytes[slot] < bytes) {
+    if (p->h_meta[slot]) (void)hipHostFree(p->h_meta[slot]);
+    p->h_meta[slot] = nullptr;
+    p->h_meta_bytes[slot] = 0;
+    const size_t want = std::max<size_t>(bytes, 1 << 20);
+    e = hipHostMalloc((void**)&p->h_meta[slot], want, hipHostMallocDefault);
+    if (e != hipSuccess) { p->h_meta[slot] = nullptr; return hip_fail(e, "hipHostMalloc(metadata)"); }
+    p->h_meta_bytes[slot] = want;
+  }
+  std::memcpy(p->h_meta[slot], src, bytes);
+  e = hipMemcpyAsync(dst, p->h_meta[slot], bytes, hipMemcpyHostToDevice, stream);
+  if (e != hipSuccess) return hip_fail(e, "hipMemcpyAsync(metadata)");
+  e = hipEventRecord(p->meta_done[slot], stream);
+  if (e != hipSuccess) return hip_fail(e, "hipEventRecord(metadata)");
+  p->meta_slot ^= 1;
+  return SLORA_OK;
 }
 
 size_t slora::segments_workspace_bytes(const slora_segments* s) { return workspace_bytes_of(s); }

@@ -15,6 +15,16 @@ namespace slora {
 void set_last_error(const char* msg);
 // Make the pool's device current (the device of its first HIP call).
 slora_status pool_device_current(slora_pool* pool);
+// What other host sources (the KV cache) read of a pool; false for NULL.
+struct PoolInfo {
+  int32_t dtype, n_classes;
+  int64_t page_bytes[2], n_pages[2];
+  char* base[2];
+};
+bool pool_info(const slora_pool* pool, PoolInfo* info);
+// Queue a copy of host bytes to dst on `stream` through the pool's pinned
+// metadata slots (src may be reused at once).
+slora_status pool_upload(slora_pool* pool, void* dst, const void* src, size_t bytes, hipStream_t stream);
 // Workspace bytes one projection of the batch needs (slora_segments_info.workspace_bytes).
 size_t segments_workspace_bytes(const slora_segments* seg);
 

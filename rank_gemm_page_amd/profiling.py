@@ -35,7 +35,8 @@ COPY_KERNEL = "__amd_rocclr_copyBuffer"
 
 def kernel_source_hash(kind: str = "fused") -> str:
     """Hash of the sources the measured kernel depends on: every host and
-    device source except the bandwidth probes and the no-allocation wrapper,
+    device source except the bandwidth probes, the no-allocation wrapper and
+    the KV cache's files (slora_kv*, which no kernel of the delta includes),
     and for the delta's kernels ("fused") not the base-plus-delta kernel's
     own file either."""
     h = hashlib.sha256()
@@ -45,6 +46,8 @@ def kernel_source_hash(kind: str = "fused") -> str:
             continue            # build by-products are not sources
         if name in ("slora_probe.hip", "slora_noalloc.hip"):
             continue            # measurement probes and a wrapper: no kernel of the delta
+        if name.startswith("slora_kv"):
+            continue            # the KV cache: its own kernels
         if kind == "fused" and name == "slora_forward.hip":
             continue
         with open(os.path.join(csrc, name), "rb") as f:
