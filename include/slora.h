@@ -474,6 +474,167 @@ slora_status slora_lora_forward_noalloc(slora_pool* pool, const slora_segments* 
 /* Message for the calling thread's last failed call ("" if none). */
 const char* slora_last_error(void);
 
+
+/* ---- KV cache in the pool, kept in 8 bits --------------------------------
+ *
+ * Keys and values of a model's attention layers in pages of the same pool as
+ * the adapters (summary page, "Unified Paging": adapter weights and KV blocks
+ * share one allocator; walkthrough step 4: KV growth is paged by it), stored
+ * as 8-bit codes with one range for each block of tokens and kv head.
+ *
+ * A page holds one block: block_tokens consecutive tokens of one sequence,
+ * one layer and one kv head, their keys and their values (2 * head_dim bytes a
+ * token).  Beside every page the cache keeps two fp32 ranges, one for the
+ * block's keys and one for its values: the largest magnitude appended to the
+ * block so far.  A code stands for
+ *
+ *     code * range / 127   (SLORA_KV_INT8: code = -127 .. 127)
+ *     code * range / 448   (SLORA_KV_FP8: code = an e4m3 number)
+ *
+ * and is the nearest one to the appended value (ties to even), computed in 64
+ * bits as value * (127 or 448 / range).  When a later append raises the range
+ * of a block that is partly filled, its older codes are coded again:
+ * nearest(code * (old range / new range)).  A value that is not finite (or,
+ * after the rotation, beyond fp32) makes the range NaN, and every key (or
+ * value) of that block and head then reads as NaN: it is never lost silently.
+ *
+ * Position p of a sequence is its p-th token (0, 1, ...).  Rotation by
+ * positions: for the pairs (a_i, b_i), i = 0 .. rot_dim/2 - 1, of a head,
+ *
+ *     a_i' = a_i cos(p, i) - b_i sin(p, i)     b_i' = b_i cos(p, i) + a_i sin(p, i)
+ *
+ * in 64 bits, rounded once; pairs are (i, i + rot_dim/2) (SLORA_KV_HALVES) or
+ * (2i, 2i + 1) (SLORA_KV_NEIGHBOURS); elements from rot_dim on stay as they
+ * are.  cos_sin is the caller's table, device fp32 [n_positions][rot_dim]: a
+ * position's rot_dim/2 cosines, then its rot_dim/2 sines.
+ *
+ * One step of a server: slora_kv_build_step names the sequences of the batch
+ * and how many tokens each one gains, slora_kv_step_upload brings the step to
+ * the device, and then for every layer slora_kv_append and slora_kv_attend run
+ * on the layer's q, k and v (between slora_lora_delta of the q, k and v
+ * projections and that of o).  The rows of a step are the new tokens of its
+ * sequences, sequence after sequence in the order given.
+ *
+ * Ordering: uploads and launches of one cache go to one stream, or the caller
+ * orders them (a launch reads the page table that earlier uploads wrote, and
+ * attention reads what earlier appends stored).  Launches may be captured into
+ * a HIP graph; uploads may not.  A replayed append stores the same positions
+ * again from what its input buffers then hold; ranges only grow. */
+typedef struct slora_kv slora_kv;
+typedef struct slora_kv_step slora_kv_step;
+
+typedef enum { SLORA_KV_INT8 = 0, SLORA_KV_FP8 = 1 } slora_kv_code;
+typedef enum { SLORA_KV_HALVES = 0, SLORA_KV_NEIGHBOURS = 1 } slora_kv_pairs;
+
+typedef struct {
+  int32_t cls;          /* page class that holds the blocks (0 or 1) */
+  int32_t code;         /* slora_kv_code */
+  int32_t n_layers;     /* 1 .. 1024 */
+  int32_t n_heads;      /* query heads, at most 1024: a multiple of n_kv_heads */
+  int32_t n_kv_heads;   /* query head h reads kv head h / (n_heads / n_kv_heads) */
+  int32_t head_dim;     /* 64, 128 or 256 */
+  int32_t block_tokens; /* a multiple of 32 with 2 * block_tokens * head_dim bytes in a page; 0: the most that fit */
+  int32_t max_seqs;     /* sequence ids are 0 .. max_seqs-1 */
+  int32_t max_tokens;   /* longest sequence */
+  int32_t rot_dim;      /* rotated elements of a head: 0 or a multiple of 16, at most head_dim */
+  int32_t rot_pairs;    /* slora_kv_pairs */
+  int32_t reserved0;    /* must be 0 */
+} slora_kv_desc;
+
+/* Bytes of device memory the cache needs beside the pages (page table, 4 bytes
+ * for each block of max_seqs x n_layers x n_kv_heads sequences of max_tokens,
+ * and the ranges, 8 bytes for each page of the class); 0 on a bad argument. */
+size_t slora_kv_device_bytes(const slora_pool* pool, const slora_kv_desc* desc);
+/* A cache over pool; dev is device memory of dev_bytes >=
+ * slora_kv_device_bytes, 16-byte aligned, that the caller keeps until after
+ * slora_kv_destroy and need not clear.  Every sequence starts empty.  Host
+ * only.  The pool's page class must give pages whose size is a multiple of
+ * 16 bytes (every class does). */
+slora_status slora_kv_create(slora_pool* pool, const slora_kv_desc* desc, void* dev, size_t dev_bytes,
+                             slora_kv** out);
+/* Returns the cache's pages to the pool; before slora_pool_destroy. */
+void slora_kv_destroy(slora_kv* kv);
+/* Empty sequence `seq`: its pages go to the tail of the pool's free list, and
+ * steps built with it become stale.  Launches that still read the pages must
+ * be ordered before whatever the caller lets write them next. */
+slora_status slora_kv_drop(slora_kv* kv, int32_t seq);
+/* Tokens of sequence `seq` (with those of every step built so far), or -1. */
+int64_t slora_kv_length(const slora_kv* kv, int32_t seq);
+/* Page ids of sequence `seq`, layer, kv head, block by block: the first
+ * min(cap, blocks) to ids (host, may be NULL when cap is 0), the count to *n. */
+slora_status slora_kv_pages(const slora_kv* kv, int32_t seq, int32_t layer, int32_t head, int32_t* ids,
+                            int32_t cap, int32_t* n);
+
+/* A step over n sequences seqs[i] (distinct ids) with counts[i] >= 0 rows each
+ * (host arrays).  reread == 0: the sequences grow by counts[i] tokens; the
+ * pages that takes are taken from the pool for every layer and kv head, all or
+ * nothing (SLORA_E_NOMEM), and the rows are the new tokens.  reread == 1:
+ * nothing grows, and the rows are the last counts[i] tokens of each sequence
+ * (at most its length); such a step is for slora_kv_read, and for attention of
+ * rows whose keys and values are stored already.  Host only. */
+slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, const int32_t* counts,
+                                 int32_t reread, slora_kv_step** out);
+void slora_kv_step_destroy(slora_kv_step* step);
+
+typedef struct {
+  int32_t n_seqs;
+  int32_t n_rows;          /* rows of the batch: q, k, v, out have n_rows tokens */
+  int32_t max_len;         /* longest sequence at the end of the step */
+  int32_t n_blocks;        /* blocks of one layer and head that the rows touch */
+  int32_t n_new_pages;     /* pages taken from the pool, over all layers and heads */
+  int32_t n_row_tiles;     /* attention tiles of 16 rows (of one kv head), counted with their key splits */
+  int32_t n_prompt_tiles;  /* attention tiles of a long run of rows */
+  int32_t reserved0;
+  size_t meta_bytes;       /* device metadata size for slora_kv_step_upload */
+  size_t workspace_bytes;  /* device workspace size for slora_kv_attend */
+} slora_kv_step_info;
+slora_status slora_kv_step_get_info(const slora_kv_step* step, slora_kv_step_info* info);
+
+/* Copy the step's tables to dev_meta (device, >= meta_bytes, 16-byte aligned,
+ * kept untouched while launches use it) and enter its pages in the cache's
+ * page table, on `stream`, without waiting.  SLORA_E_STALE if a sequence of the
+ * step was dropped since. */
+slora_status slora_kv_step_upload(slora_kv_step* step, void* dev_meta, size_t dev_meta_bytes, void* stream);
+
+/* Append the step's rows in `layer`: rotate k and store k and v into the
+ * blocks, and, where q is given, write its rotated rows to q_out.  q, k, v and
+ * q_out are device memory of the pool dtype, [n_rows] tokens of [heads][head_dim]
+ * contiguous elements, token t at t * stride elements (so that q, k and v may be
+ * parts of one projection's output); pointers are 16-byte aligned and strides
+ * are multiples of 16 bytes and at least heads * head_dim.  q_out may be q
+ * itself (same pointer and stride), else they do not overlap; q and q_out may
+ * both be NULL.  cos_sin holds every position of the step (n_positions >
+ * the largest one); without rotation (rot_dim 0) it may be NULL.  One launch on
+ * `stream`.  A reread step is refused. */
+slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* step, int32_t layer, const void* q,
+                             int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                             int64_t k_stride, const void* v, int64_t v_stride, const float* cos_sin,
+                             int64_t n_positions, void* stream);
+
+/* Attention of the step's rows in `layer` over the cached tokens: for row t at
+ * position p of its sequence and query head h,
+ *
+ *     s_j = scale * q[t, h] . k_j      out[t, h] = sum_j softmax(s)_j v_j
+ *
+ * over positions j <= p, with window > 0 also j > p - window (0: no window).
+ * k and v are the cached values; products are accumulated in fp32, the softmax
+ * is held in fp32, and out is rounded once to the pool dtype.  q is [n_rows]
+ * rotated rows (slora_kv_append's q_out), q and out laid out as for
+ * slora_kv_append.  workspace is device memory of at least workspace_bytes,
+ * 16-byte aligned (may be NULL when that is 0); launches that may run at the
+ * same time need workspaces of their own.  Launches on `stream` and returns without waiting. */
+slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* step, int32_t layer, const void* q,
+                             int64_t q_stride, void* out, int64_t out_stride, float scale, int32_t window,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Read the cached keys and values of the step's rows in `layer` back, as the
+ * values their codes stand for (keys as they were stored: rotated), rounded
+ * once to the pool dtype: what a sequence is made of when it leaves for the
+ * host or another cache.  k and v (either may be NULL) are laid out as for
+ * slora_kv_append and written. */
+slora_status slora_kv_read(slora_kv* kv, const slora_kv_step* step, int32_t layer, void* k, int64_t k_stride,
+                           void* v, int64_t v_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,9 @@ SLORA_MFMA_MAX_RANK = 64          # segments of higher rank always take the vect
 SLORA_TUNE_MFMA_SHRINK_SPLITS, SLORA_TUNE_FUSED, SLORA_TUNE_XCDS, SLORA_TUNE_TILE_ORDER = 3, 4, 5, 6
 SLORA_TUNE_FWD_GROUP, SLORA_TUNE_FWD_TILE, SLORA_TUNE_SHRINK_ROWS, SLORA_TUNE_FWD_KSPLIT = 7, 8, 9, 10
 
+SLORA_KV_INT8, SLORA_KV_FP8 = 0, 1
+SLORA_KV_HALVES, SLORA_KV_NEIGHBOURS = 0, 1
+
 EXPORTED = [
     "slora_pool_create", "slora_pool_destroy", "slora_pool_set_tuning", "slora_alloc_pages",
     "slora_free_pages", "slora_free_count", "slora_load_adapter", "slora_unload_adapter",
@@ -39,6 +42,9 @@ EXPORTED = [
     "slora_lora_forward", "slora_lora_forward_timed", "slora_last_error",
     "slora_lora_delta_multi", "slora_lora_delta_multi_timed", "slora_lora_forward_noalloc",
     "slora_segments_forward_tables",
+    "slora_kv_device_bytes", "slora_kv_create", "slora_kv_destroy", "slora_kv_drop", "slora_kv_length",
+    "slora_kv_pages", "slora_kv_build_step", "slora_kv_step_destroy", "slora_kv_step_get_info",
+    "slora_kv_step_upload", "slora_kv_append", "slora_kv_attend", "slora_kv_read",
 ]
 # include/slora_probe.h: bandwidth probes (measurement only)
 EXPORTED_PROBE = ["slora_probe_read", "slora_probe_gather"]
@@ -63,6 +69,26 @@ class SegmentsInfo(ctypes.Structure):
                 ("n_shrink_tiles", c_int32), ("n_expand_tiles", c_int32),
                 ("n_mfma_segments", c_int32), ("n_combine_tiles", c_int32), ("meta_bytes", c_size_t),
                 ("workspace_bytes", c_size_t)]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [(name, c_int32) for name in
+                ("cls", "code", "n_layers", "n_heads", "n_kv_heads", "head_dim", "block_tokens", "max_seqs",
+                 "max_tokens", "rot_dim", "rot_pairs", "reserved0")]
+
+
+class KvStepInfo(ctypes.Structure):
+    _fields_ = [(name, c_int32) for name in
+                ("n_seqs", "n_rows", "max_len", "n_blocks", "n_new_pages", "n_row_tiles", "n_prompt_tiles",
+                 "reserved0")] + [("meta_bytes", c_size_t), ("workspace_bytes", c_size_t)]
+
+
+class KvCache(c_void_p):
+    """Handle of a cache; ``desc`` holds its description."""
+
+
+class KvStep(c_void_p):
+    """Handle of a step; ``kv`` is its cache and ``n_rows`` its rows."""
 
 
 _LIB = None
@@ -116,6 +142,21 @@ def lib():
             "slora_lora_forward_noalloc": (c_int32, [P, P, c_int32, P, P, P, P]),
             "slora_segments_forward_tables": (c_int32, [P, POINTER(c_int32), POINTER(c_int32), c_size_t,
                                                         POINTER(c_int32), c_size_t]),
+            "slora_kv_device_bytes": (c_size_t, [P, POINTER(KvDesc)]),
+            "slora_kv_create": (c_int32, [P, POINTER(KvDesc), P, c_size_t, POINTER(KvCache)]),
+            "slora_kv_destroy": (None, [P]),
+            "slora_kv_drop": (c_int32, [P, c_int32]),
+            "slora_kv_length": (c_int64, [P, c_int32]),
+            "slora_kv_pages": (c_int32, [P, c_int32, c_int32, c_int32, POINTER(c_int32), c_int32, POINTER(c_int32)]),
+            "slora_kv_build_step": (c_int32, [P, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32,
+                                              POINTER(KvStep)]),
+            "slora_kv_step_destroy": (None, [P]),
+            "slora_kv_step_get_info": (c_int32, [P, POINTER(KvStepInfo)]),
+            "slora_kv_step_upload": (c_int32, [P, P, c_size_t, P]),
+            "slora_kv_append": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, P, c_int64, P, c_int64, P, c_int64,
+                                          P]),
+            "slora_kv_attend": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, c_float, c_int32, P, c_size_t, P]),
+            "slora_kv_read": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, P]),
             "slora_probe_read": (c_int32, [P, c_int64, c_int32, c_int32, P, P, P, P]),
             "slora_probe_gather": (c_int32, [P, c_int64, c_int64, P, c_int64, P, c_int64, c_int64, P,
                                              c_int64, c_int32, P, P, P, P]),
@@ -448,3 +489,115 @@ def slora_segments_forward_tables(seg):
     return (L, rb[:2 * L["n_rb"]].reshape(-1, 2),
             st[:L["n_proj"] * L["n_stages"] * L["stage_words"]].reshape(L["n_proj"], L["n_stages"],
                                                                           L["stage_words"]))
+
+
+# -- KV cache in the pool ------------------------------------------------------
+
+def slora_kv_device_bytes(pool, **desc) -> int:
+    """desc: the fields of slora_kv_desc by name (those left out are 0)."""
+    n = int(lib().slora_kv_device_bytes(pool, ctypes.byref(KvDesc(**desc))))
+    if n == 0:
+        _check(SLORA_E_INVAL, "slora_kv_device_bytes")
+    return n
+
+
+def slora_kv_create(pool, dev, dev_bytes: int, **desc) -> KvCache:
+    kv = KvCache()
+    kv.desc = KvDesc(**desc)
+    _check(lib().slora_kv_create(pool, ctypes.byref(kv.desc), _ptr(dev), int(dev_bytes), ctypes.byref(kv)),
+           "slora_kv_create")
+    return kv
+
+
+def slora_kv_destroy(kv) -> None:
+    lib().slora_kv_destroy(kv)
+
+
+def slora_kv_drop(kv, seq: int) -> None:
+    _check(lib().slora_kv_drop(kv, seq), "slora_kv_drop")
+
+
+def slora_kv_length(kv, seq: int) -> int:
+    return int(lib().slora_kv_length(kv, seq))
+
+
+def slora_kv_pages(kv, seq: int, layer: int = 0, head: int = 0) -> np.ndarray:
+    n = c_int32()
+    _check(lib().slora_kv_pages(kv, seq, layer, head, None, 0, ctypes.byref(n)), "slora_kv_pages")
+    ids = np.empty(max(n.value, 1), dtype=np.int32)
+    _check(lib().slora_kv_pages(kv, seq, layer, head, _i32p(ids), n.value, ctypes.byref(n)), "slora_kv_pages")
+    return ids[:n.value]
+
+
+def slora_kv_build_step(kv, seqs, counts, reread: bool = False) -> KvStep:
+    seqs = np.ascontiguousarray(seqs, dtype=np.int32)
+    counts = np.ascontiguousarray(counts, dtype=np.int32)
+    if seqs.ndim != 1 or seqs.shape != counts.shape:
+        raise ValueError("one count per sequence")
+    step = KvStep()
+    _check(lib().slora_kv_build_step(kv, seqs.size, _i32p(seqs) if seqs.size else None,
+                                     _i32p(counts) if seqs.size else None, int(reread), ctypes.byref(step)),
+           "slora_kv_build_step")
+    step.kv, step.n_rows = kv, int(counts.sum(dtype=np.int64))
+    return step
+
+
+def slora_kv_step_destroy(step) -> None:
+    lib().slora_kv_step_destroy(step)
+
+
+def slora_kv_step_get_info(step) -> dict:
+    info = KvStepInfo()
+    _check(lib().slora_kv_step_get_info(step, ctypes.byref(info)), "slora_kv_step_get_info")
+    return {name: getattr(info, name) for name, _ in KvStepInfo._fields_ if name != "reserved0"}
+
+
+def slora_kv_step_upload(step, dev_meta, dev_meta_bytes: int, stream=None) -> None:
+    _check(lib().slora_kv_step_upload(step, _ptr(dev_meta), int(dev_meta_bytes), _stream(stream)),
+           "slora_kv_step_upload")
+
+
+def _rows(x, step, heads: int, stride):
+    """(address, stride in elements between tokens) of a [n_rows, heads, head_dim] operand: a tensor of that shape
+    whose heads are contiguous, or a raw address with its stride (contiguous by default)."""
+    dim = step.kv.desc.head_dim
+    if x is None:
+        return 0, 0
+    if hasattr(x, "stride") and hasattr(x, "shape"):
+        if tuple(x.shape[1:]) != (heads, dim) or x.shape[0] < step.n_rows:
+            raise ValueError(f"expected at least {step.n_rows} rows of {heads} heads of {dim}, got {tuple(x.shape)}")
+        if x.shape[0] and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim)):
+            raise ValueError("the heads of a row must be contiguous")
+        if stride is None and x.shape[0] > 1:
+            stride = x.stride(0)
+    return _ptr(x), heads * dim if stride is None else int(stride)
+
+
+def slora_kv_append(kv, step, layer: int, k, v, q=None, q_out=None, cos_sin=None, stream=None, k_stride=None,
+                    v_stride=None, q_stride=None, q_out_stride=None, n_positions=None) -> None:
+    """cos_sin: a contiguous fp32 tensor [n_positions, rot_dim], or a raw address with n_positions."""
+    d = kv.desc
+    if cos_sin is not None and n_positions is None:
+        if cos_sin.dim() != 2 or cos_sin.shape[1] != d.rot_dim or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous [n_positions, rot_dim] tensor")
+        n_positions = cos_sin.shape[0]
+    qp, qs = _rows(q, step, d.n_heads, q_stride)
+    op, os_ = _rows(q_out, step, d.n_heads, q_out_stride)
+    kp, ks = _rows(k, step, d.n_kv_heads, k_stride)
+    vp, vs = _rows(v, step, d.n_kv_heads, v_stride)
+    _check(lib().slora_kv_append(kv, step, layer, qp, qs, op, os_, kp, ks, vp, vs, _ptr(cos_sin), n_positions or 0,
+                                 _stream(stream)), "slora_kv_append")
+
+
+def slora_kv_attend(kv, step, layer: int, q, out, scale: float, window: int = 0, workspace=None,
+                    workspace_bytes: int = 0, stream=None, q_stride=None, out_stride=None) -> None:
+    qp, qs = _rows(q, step, kv.desc.n_heads, q_stride)
+    op, os_ = _rows(out, step, kv.desc.n_heads, out_stride)
+    _check(lib().slora_kv_attend(kv, step, layer, qp, qs, op, os_, scale, window, _ptr(workspace),
+                                 int(workspace_bytes), _stream(stream)), "slora_kv_attend")
+
+
+def slora_kv_read(kv, step, layer: int, k=None, v=None, stream=None, k_stride=None, v_stride=None) -> None:
+    kp, ks = _rows(k, step, kv.desc.n_kv_heads, k_stride)
+    vp, vs = _rows(v, step, kv.desc.n_kv_heads, v_stride)
+    _check(lib().slora_kv_read(kv, step, layer, kp, ks, vp, vs, _stream(stream)), "slora_kv_read")
