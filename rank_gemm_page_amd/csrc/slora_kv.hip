@@ -41,7 +41,12 @@ template <> struct Code<SLORA_KV_INT8> {
     return r;
   }
   static __device__ __forceinline__ float value(uint32_t byte) { return (float)(int)byte - 128.f; }
-  static __device__ __forceinline__ uint32_t nearest(double x) { return (uint32_t)((int)__builtin_rint(x) + 128) & 0xFF; }
+  // Added to 1.5 * 2^52, a number this small is rounded to an integer (ties to
+  // even) that stands in the low bits.
+  static __device__ __forceinline__ uint32_t nearest(double x) {
+#pragma clang fp contract(off)
+    return (uint32_t)__double2loint(x + (0x1.8p52 + 128.)) & 0xFF;
+  }
 };
 
 template <> struct Code<SLORA_KV_FP8> {
@@ -88,110 +93,191 @@ __global__ __launch_bounds__(kThreads) void kv_patch_kernel(int32_t* table, cons
 }
 
 // ---------------------------------------------------------------------------
-// Append.
+// Elements in memory, 8 or 4 at a time.
 
-// Element d of a row rotated by the angles cs (cosines, then sines): products
-// of an fp16 or fp32 element and an fp32 cosine are exact in 64 bits, so the
-// result is rounded once whether or not the compiler fuses them.
-template <typename T>
-__device__ __forceinline__ double rotated(const T* row, const float* cs, int d, int rot, int pairs) {
-  const double x = (double)(float)row[d];
-  if (d >= rot) return x;
-  const int half = rot >> 1;
-  int i, o;
-  bool second;
-  if (pairs == SLORA_KV_HALVES) {
-    second = d >= half;
-    i = second ? d - half : d;
-    o = second ? i : d + half;
-  } else {
-    second = d & 1;
-    i = d >> 1;
-    o = d ^ 1;
-  }
-  const double c = cs[i], s = cs[half + i], y = (double)(float)row[o];
-  return second ? x * c + y * s : x * c - y * s;
+template <typename T> struct Vec;
+template <> struct Vec<_Float16> {
+  typedef half8 v8;
+  typedef _Float16 v4 __attribute__((ext_vector_type(4)));
+};
+template <> struct Vec<float> {
+  typedef float8v v8;
+  typedef float4v v4;
+};
+
+// A 64-bit number rounded once.  fp16: to fp32 with the last bit set where
+// that was inexact (rounding to odd), which the rounding to fp16 then sees.
+__device__ __forceinline__ void round_to(double r, float* y) { *y = (float)r; }
+__device__ __forceinline__ void round_to(double r, _Float16* y) {
+  const float f = (float)r;
+  const double back = (double)f;
+  uint32_t bits = __float_as_uint(f);
+  if (back != r && !(bits & 1)) bits += __builtin_fabs(back) < __builtin_fabs(r) ? 1u : ~0u;
+  *y = (_Float16)__uint_as_float(bits);
 }
 
-// Largest of the workgroup's values (bit patterns of non-negative floats order
-// as integers, with infinities and NaN above every finite one).
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* lds) {
+// Unit u of a row is eight of its pairs (a, b): of the rotated part, and behind
+// it, turned by no angle, elements 16u .. 16u + 15 as pairs of neighbours
+// (halves: of 8 and 8).  Their elements lie in two runs of 8.
+template <typename T> struct Pairs { typename Vec<T>::v8 a, b; };
+struct Turn { float8v c, s; };
+
+__device__ __forceinline__ void unit_runs(const KvView& kv, int u, int* a, int* b) {
+  const bool split = kv.pairs == SLORA_KV_HALVES && u * 16 < kv.rot;
+  *a = split ? u * 8 : u * 16;
+  *b = split ? (kv.rot >> 1) + u * 8 : u * 16 + 8;
+}
+template <typename T>
+__device__ __forceinline__ Pairs<T> load_pairs(const KvView& kv, const T* head, int a, int b) {
+  typedef typename Vec<T>::v8 V;
+  const V x = *reinterpret_cast<const V*>(head + a), y = *reinterpret_cast<const V*>(head + b);
+  if (kv.pairs == SLORA_KV_HALVES) return {x, y};
+  return {__builtin_shufflevector(x, y, 0, 2, 4, 6, 8, 10, 12, 14), __builtin_shufflevector(x, y, 1, 3, 5, 7, 9, 11, 13, 15)};
+}
+__device__ __forceinline__ Turn load_turn(const KvView& kv, const float* cos_sin, int64_t pos, int u) {
+  if (u * 16 >= kv.rot) return {float8v{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, float8v{}};
+  const float* row = cos_sin + pos * kv.rot + u * 8;
+  return {*reinterpret_cast<const float8v*>(row), *reinterpret_cast<const float8v*>(row + (kv.rot >> 1))};
+}
+// Products of an fp16 or fp32 element and an fp32 cosine are exact in 64 bits,
+// so the result is rounded once whether or not the compiler fuses them.
+__device__ __forceinline__ void turned(float a, float b, float c, float s, double* ra, double* rb) {
+  *ra = (double)a * c - (double)b * s;
+  *rb = (double)b * c + (double)a * s;
+}
+
+// 4 x 4 bytes across four lanes: lane k of a quad gets byte k of lanes 0 .. 3.
+__device__ __forceinline__ uint32_t quad_transpose(uint32_t x, int lane) {
+  uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true);       // lane ^ 1
+  x = __builtin_amdgcn_perm(y, x, lane & 1 ? 0x03070105u : 0x06020400u);
+  y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true);                // lane ^ 2
+  return __builtin_amdgcn_perm(y, x, lane & 2 ? 0x03020706u : 0x05040100u);
+}
+
+// ---------------------------------------------------------------------------
+// Append.  An item is one touched block of one kv head.  Blocks that gain few
+// tokens are a wave's work, the others a workgroup's.
+//
+// Keys go in units of 8 pairs of a token; values in the page's 16-byte units (2
+// elements of 8 tokens), read token by token, 4 elements a lane, and turned by
+// byte transposes across four lanes.  The first pass finds the largest
+// magnitudes and keeps one unit of each a thread in registers (all there is
+// where a page holds 8 KiB); what is beyond them is read again by the second
+// pass, which writes the codes.
+
+// Bit patterns of non-negative floats order as integers, with infinities and
+// NaN above every finite one.
+__device__ __forceinline__ uint32_t magnitude(double x) { return __float_as_uint(fabsf((float)x)); }
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(fabsf(x)); }
+
+template <int NT>
+__device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* lds) {
 #pragma unroll
   for (int m = 32; m; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+  if (NT == 64) return v;
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = lds[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) v = max(v, lds[w]);
-  __syncthreads();
+  for (int w = 0; w < NT / 64; ++w) v = max(v, lds[w]);
   return v;
 }
 
-__device__ __forceinline__ uint32_t magnitude(double x) { return __float_as_uint(fabsf((float)x)); }
+template <int CODE>
+__device__ __forceinline__ uint32_t again4(uint32_t old, double ratio) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w |= Code<CODE>::nearest((double)Code<CODE>::value((old >> (8 * j)) & 0xFF) * ratio) << (8 * j);
+  return w;
+}
+template <int CODE>
+__device__ __forceinline__ uint4 again16(uint4 o, double ratio) {
+  return make_uint4(again4<CODE>(o.x, ratio), again4<CODE>(o.y, ratio), again4<CODE>(o.z, ratio), again4<CODE>(o.w, ratio));
+}
 
-// One workgroup per touched block and kv head: the largest magnitudes of the
-// block's new keys and values, then the codes, 16 bytes of the page layout a
-// thread.  Workgroups behind those rotate q, 16 elements a thread.
-template <typename T, int CODE>
-__global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
+// Elements of a value unit as they are read: [8-token half][16-element half].
+template <typename T> struct Values { typename Vec<T>::v4 x[2][2]; };
+
+template <typename T, int CODE, int NT>
+__device__ __forceinline__ void store_item(const KvAppend& A, int64_t item, int tid, uint32_t* lds) {
   using C = Code<CODE>;
+  typedef typename Vec<T>::v4 V4;
   const KvView& kv = A.kv;
-  const int dim = kv.dim, tid = threadIdx.x;
-  __shared__ uint32_t lds[kThreads / 64];
-  const int64_t stores = (int64_t)A.n_blocks * kv.n_kv;
-  if (blockIdx.x >= stores) {
-    // units of 16 elements: 8 pairs of the rotated part, or 16 elements behind it
-    const int per = dim / 16;
-    const int64_t u = (blockIdx.x - stores) * kThreads + tid;
-    const int64_t head = u / per;
-    const int unit = (int)(u % per), row = (int)(head / kv.n_heads), h = (int)(head % kv.n_heads);
-    if (row >= A.n_rows) return;
-    const T* x = (const T*)A.q + row * A.q_stride + h * dim;
-    T* y = (T*)A.q_out + row * A.q_out_stride + h * dim;
-    const float* cs = A.cos_sin + (int64_t)A.row_pos[row] * kv.rot;
-    const int half = kv.rot >> 1;
-    double r[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int d = unit * 16 >= kv.rot ? unit * 16 + j
-                    : kv.pairs == SLORA_KV_HALVES ? (j < 8 ? unit * 8 + j : half + unit * 8 + j - 8) : unit * 16 + j;
-      r[j] = rotated(x, cs, d, kv.rot, kv.pairs);
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int d = unit * 16 >= kv.rot ? unit * 16 + j
-                    : kv.pairs == SLORA_KV_HALVES ? (j < 8 ? unit * 8 + j : half + unit * 8 + j - 8) : unit * 16 + j;
-      y[d] = (T)r[j];
-    }
-    return;
-  }
-  const KvBlock blk = A.blocks[blockIdx.x / kv.n_kv];
-  const int head = blockIdx.x % kv.n_kv;
+  const int dim = kv.dim, lane = tid & 63;
+  const KvBlock blk = A.blocks[item / kv.n_kv];
+  const int head = (int)(item % kv.n_kv);
   const KvSeq sq = A.seqs[blk.s];
   const int32_t page = kv_row(kv, sq.seq, A.layer, head)[blk.block];
-  char* kbase = kv.base + (int64_t)page * kv.page_bytes;
-  char* vbase = kbase + (int64_t)kv.block * dim;
+  uint8_t* kbase = (uint8_t*)kv.base + (int64_t)page * kv.page_bytes;
+  uint8_t* vbase = kbase + (int64_t)kv.block * dim;
   float* range = kv.range + 2 * (int64_t)page;
   const int pos0 = blk.block * kv.block;                       // position of slot 0
   const int64_t row0 = (int64_t)sq.row0 + pos0 - sq.start;     // batch row of slot 0 (negative before the first new slot)
-  const int count = blk.slot1 - blk.slot0;
   const T* kin = (const T*)A.k + (int64_t)head * dim;
   const T* vin = (const T*)A.v + (int64_t)head * dim;
-
-  uint32_t mk = 0, mv = 0;
-  for (int i = tid; i < count * dim; i += kThreads) {
-    const int slot = blk.slot0 + i / dim, d = i % dim;
-    const T* krow = kin + (row0 + slot) * A.k_stride;
-    mk = max(mk, magnitude(rotated(krow, A.cos_sin + (int64_t)(pos0 + slot) * kv.rot, d, kv.rot, kv.pairs)));
-    mv = max(mv, magnitude((double)(float)vin[(row0 + slot) * A.v_stride + d]));
-  }
-  mk = block_max(mk, lds);
-  mv = block_max(mv, lds);
+  const int ush = 27 - __clz(dim);                             // log2 of the units of a token (dim / 16)
+  const int units_k = (blk.slot1 - blk.slot0) << ush;
+  const int group0 = blk.slot0 >> 5, group1 = (blk.slot1 + 31) >> 5;
+  const int units_v = (group1 - group0) << (ush + 5);          // a multiple of 64: a wave's lanes act alike
+  const int g = lane >> 4, quad = (lane >> 2) & 3, k4 = lane & 3;
   const uint32_t held_k = blk.slot0 ? __float_as_uint(range[0]) & 0x7FFFFFFFu : 0;
   const uint32_t held_v = blk.slot0 ? __float_as_uint(range[1]) & 0x7FFFFFFFu : 0;
-  __syncthreads();
-  mk = max(mk, held_k);
-  mv = max(mv, held_v);
+
+  auto key = [&](int u, Pairs<T>* x, Turn* t) {
+    const int slot = blk.slot0 + (u >> ush), c = u & ((1 << ush) - 1);
+    int a, b;
+    unit_runs(kv, c, &a, &b);
+    *x = load_pairs(kv, kin + (row0 + slot) * A.k_stride, a, b);
+    *t = load_turn(kv, A.cos_sin, pos0 + slot, c);
+  };
+  auto key_max = [&](const Pairs<T>& x, const Turn& t) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      double ra, rb;
+      turned((float)x.a[j], (float)x.b[j], t.c[j], t.s[j], &ra, &rb);
+      m = max(m, max(magnitude(ra), magnitude(rb)));
+    }
+    return m;
+  };
+  auto value = [&](int u, Values<T>* x) {
+    const int group = group0 + (u >> (ush + 5)), e = (u >> 6) & ((1 << (ush - 1)) - 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int slot = group * 32 + h * 16 + g * 4 + k4;
+      x->x[h][0] = x->x[h][1] = V4{};
+      if (slot >= blk.slot0 && slot < blk.slot1) {
+        const T* row = vin + (row0 + slot) * A.v_stride + e * 32 + quad * 4;
+        x->x[h][0] = *reinterpret_cast<const V4*>(row);
+        x->x[h][1] = *reinterpret_cast<const V4*>(row + 16);
+      }
+    }
+  };
+  auto value_max = [&](const Values<T>& x) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int n = 0; n < 16; ++n) m = max(m, magnitude((float)x.x[n >> 3][(n >> 2) & 1][n & 3]));
+    return m;
+  };
+
+  Pairs<T> kx{};
+  Turn kt{};
+  Values<T> vx{};
+  if (tid < units_v) value(tid, &vx);
+  if (tid < units_k) key(tid, &kx, &kt);
+  uint32_t mk = key_max(kx, kt), mv = value_max(vx);
+  for (int u = tid + NT; u < units_k; u += NT) {
+    Pairs<T> x;
+    Turn t;
+    key(u, &x, &t);
+    mk = max(mk, key_max(x, t));
+  }
+  for (int u = tid + NT; u < units_v; u += NT) {
+    Values<T> x;
+    value(u, &x);
+    mv = max(mv, value_max(x));
+  }
+  mk = max(team_max<NT>(mk, lds), held_k);
+  mv = max(team_max<NT>(mv, lds + NT / 64), held_v);
   const bool bad_k = mk >= 0x7F800000u, bad_v = mv >= 0x7F800000u;
   if (tid == 0) {
     range[0] = bad_k ? __uint_as_float(0x7FC00000u) : __uint_as_float(mk);
@@ -199,57 +285,143 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
   }
   const double new_k = __uint_as_float(mk), new_v = __uint_as_float(mv);
   const double inv_k = mk ? (double)C::kTop / new_k : 0., inv_v = mv ? (double)C::kTop / new_v : 0.;
-  const double again_k = mk ? (double)__uint_as_float(held_k) / new_k : 0.;
-  const double again_v = mv ? (double)__uint_as_float(held_v) / new_v : 0.;
+  constexpr uint32_t kZero4 = C::kZero * 0x01010101u;
 
-  // keys: a 16-byte unit is 16 elements of one slot
-  const int first_k = mk != held_k ? 0 : blk.slot0;
-  for (int u = tid; u < (blk.slot1 - first_k) * (dim / 16); u += kThreads) {
-    const int slot = first_k + u / (dim / 16), d0 = u % (dim / 16) * 16;
-    uint8_t* at = (uint8_t*)kbase + kv_k_byte(slot, d0, dim);
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (slot >= blk.slot0) {
-      const T* krow = kin + (row0 + slot) * A.k_stride;
-      const float* cs = A.cos_sin + (int64_t)(pos0 + slot) * kv.rot;
+  // keys
+  auto put_key = [&](int u, const Pairs<T>& x, const Turn& t) {
+    const int slot = blk.slot0 + (u >> ush), c = u & ((1 << ush) - 1);
+    int a, b;
+    unit_runs(kv, c, &a, &b);
+    uint32_t wa[2] = {0, 0}, wb[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        w[j >> 2] |= (bad_k ? C::kZero : C::nearest(rotated(krow, cs, d0 + j, kv.rot, kv.pairs) * inv_k)) << (8 * (j & 3));
-    } else {
-      const uint4 old = ld16(at);
-      const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+    for (int j = 0; j < 8; ++j) {
+      double ra, rb;
+      turned((float)x.a[j], (float)x.b[j], t.c[j], t.s[j], &ra, &rb);
+      wa[j >> 2] |= C::nearest(ra * inv_k) << (8 * (j & 3));
+      wb[j >> 2] |= C::nearest(rb * inv_k) << (8 * (j & 3));
+    }
+    uint2 first = make_uint2(wa[0], wa[1]), second = make_uint2(wb[0], wb[1]);
+    if (kv.pairs == SLORA_KV_NEIGHBOURS) {
+      first = make_uint2(__builtin_amdgcn_perm(wb[0], wa[0], 0x05010400u), __builtin_amdgcn_perm(wb[0], wa[0], 0x07030602u));
+      second = make_uint2(__builtin_amdgcn_perm(wb[1], wa[1], 0x05010400u), __builtin_amdgcn_perm(wb[1], wa[1], 0x07030602u));
+    }
+    if (bad_k) first = second = make_uint2(kZero4, kZero4);
+    *reinterpret_cast<uint2*>(kbase + kv_k_byte(slot, a, dim)) = first;
+    *reinterpret_cast<uint2*>(kbase + kv_k_byte(slot, b, dim)) = second;
+  };
+  if (tid < units_k) put_key(tid, kx, kt);
+  for (int u = tid + NT; u < units_k; u += NT) {
+    Pairs<T> x;
+    Turn t;
+    key(u, &x, &t);
+    put_key(u, x, t);
+  }
+  if (blk.slot0 && mk != held_k) {                             // the range grew: older keys are coded again
+    const double ratio = bad_k ? 0. : (double)__uint_as_float(held_k) / new_k;
+    for (int u = tid; u < blk.slot0 << ush; u += NT) {
+      uint8_t* at = kbase + kv_k_byte(u >> ush, (u & ((1 << ush) - 1)) * 16, dim);
+      st16(at, again16<CODE>(ld16(at), ratio));
+    }
+  }
+
+  // values
+  const bool grew = blk.slot0 && mv != held_v;
+  const double ratio = grew && !bad_v ? (double)__uint_as_float(held_v) / new_v : 0.;
+  auto put_value = [&](int u, const Values<T>& x) {
+    const int group = group0 + (u >> (ush + 5)), e = (u >> 6) & ((1 << (ush - 1)) - 1);
+    uint32_t w[4], mask[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        w[j >> 2] |= (bad_k ? C::kZero : C::nearest((double)C::value((o[j >> 2] >> (8 * (j & 3))) & 0xFF) * again_k))
-                     << (8 * (j & 3));
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int slot = group * 32 + h * 16 + g * 4 + b;
+        if (slot >= blk.slot0 && slot < blk.slot1) mask[h] |= 0xFFu << (8 * b);
+      }
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c |= C::nearest((double)(float)x.x[h][d][j] * inv_v) << (8 * j);
+        w[2 * d + h] = quad_transpose(bad_v ? kZero4 : c, lane);
+      }
+    }
+    uint8_t* at = vbase + ((int64_t)group << (ush + 9)) + e * 1024 + lane * 16;
+    if ((mask[0] & mask[1]) != 0xFFFFFFFFu) {
+      if (!(mask[0] | mask[1]) && !grew) return;
+      uint4 old = ld16(at);
+      if (grew) old = again16<CODE>(old, ratio);
+      w[0] = (w[0] & mask[0]) | (old.x & ~mask[0]);
+      w[1] = (w[1] & mask[1]) | (old.y & ~mask[1]);
+      w[2] = (w[2] & mask[0]) | (old.z & ~mask[0]);
+      w[3] = (w[3] & mask[1]) | (old.w & ~mask[1]);
     }
     st16(at, make_uint4(w[0], w[1], w[2], w[3]));
+  };
+  if (tid < units_v) put_value(tid, vx);
+  for (int u = tid + NT; u < units_v; u += NT) {
+    Values<T> x;
+    value(u, &x);
+    put_value(u, x);
   }
-  // values: a 16-byte unit is 2 elements of 8 slots
-  const int first_v = (mv != held_v ? 0 : blk.slot0) / 32;
-  const int groups = (blk.slot1 + 31) / 32 - first_v;
-  for (int u = tid; u < groups * dim * 2; u += kThreads) {
-    const int group = first_v + u / (dim * 2), lane = u % 64, e = u % (dim * 2) / 64;
-    const int g = lane >> 4, i = lane & 15;
-    uint8_t* at = (uint8_t*)vbase + (int64_t)group * 32 * dim + e * 1024 + lane * 16;
-    const uint4 old = ld16(at);
-    const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-    uint32_t w[4];
-    bool any = false;
-#pragma unroll
-    for (int b = 0; b < 16; ++b) {
-      const int j = b & 7, d = e * 32 + (b >> 3) * 16 + i;
-      const int slot = group * 32 + (j >> 2) * 16 + g * 4 + (j & 3);
-      uint32_t byte = (o[b >> 2] >> (8 * (b & 3))) & 0xFF;
-      if (slot >= blk.slot0 && slot < blk.slot1) {
-        any = true;
-        byte = bad_v ? C::kZero : C::nearest((double)(float)vin[(row0 + slot) * A.v_stride + d] * inv_v);
-      } else if (slot < blk.slot0 && mv != held_v) {
-        any = true;
-        byte = bad_v ? C::kZero : C::nearest((double)C::value(byte) * again_v);
-      }
-      w[b >> 2] = (b & 3 ? w[b >> 2] : 0) | byte << (8 * (b & 3));
+  if (grew)
+    for (int u = tid; u < group0 << (ush + 5); u += NT) {
+      uint8_t* at = vbase + (int64_t)u * 16;
+      st16(at, again16<CODE>(ld16(at), ratio));
     }
-    if (any) st16(at, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// Workgroups: items a wave each (A.n_small blocks), items a workgroup each,
+// then q: a thread rotates one unit of A.q_heads heads of a row, so that a
+// row's angles are read once for them.
+template <typename T, int CODE>
+__global__ __launch_bounds__(kThreads, 4) void kv_append_kernel(KvAppend A) {
+  typedef typename Vec<T>::v8 V8;
+  const KvView& kv = A.kv;
+  __shared__ uint32_t lds[2 * kThreads / 64];
+  const int tid = threadIdx.x;
+  const int64_t small = (int64_t)A.n_small * kv.n_kv, small_wgs = (small + 3) / 4;
+  const int64_t wgs = small_wgs + (int64_t)(A.n_blocks - A.n_small) * kv.n_kv;
+  if (blockIdx.x < small_wgs) {
+    const int64_t item = (int64_t)blockIdx.x * 4 + (tid >> 6);
+    if (item < small) store_item<T, CODE, 64>(A, item, tid & 63, nullptr);
+    return;
+  }
+  if (blockIdx.x < wgs) {
+    store_item<T, CODE, kThreads>(A, small + blockIdx.x - small_wgs, tid, lds);
+    return;
+  }
+  const int per = kv.dim / 16, chunks = (kv.n_heads + A.q_heads - 1) / A.q_heads;
+  const int64_t i = (blockIdx.x - wgs) * kThreads + tid, rc = i / per;
+  const int u = (int)(i - rc * per), row = (int)(rc / chunks), h0 = (int)(rc - (int64_t)row * chunks) * A.q_heads;
+  if (row >= A.n_rows) return;
+  int a, b;
+  unit_runs(kv, u, &a, &b);
+  const bool turns = u * 16 < kv.rot;
+  const Turn t = load_turn(kv, A.cos_sin, A.row_pos[row], u);
+  const T* in = (const T*)A.q + row * A.q_stride;
+  T* out = (T*)A.q_out + row * A.q_out_stride;
+  const int h1 = min(kv.n_heads, h0 + A.q_heads);
+  for (int h = h0; h < h1; ++h) {
+    Pairs<T> x = load_pairs(kv, in + h * kv.dim, a, b);
+    if (turns) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        double ra, rb;
+        turned((float)x.a[j], (float)x.b[j], t.c[j], t.s[j], &ra, &rb);
+        T ya, yb;
+        round_to(ra, &ya);
+        round_to(rb, &yb);
+        x.a[j] = ya;
+        x.b[j] = yb;
+      }
+    }
+    V8 first = x.a, second = x.b;
+    if (kv.pairs == SLORA_KV_NEIGHBOURS) {
+      first = __builtin_shufflevector(x.a, x.b, 0, 8, 1, 9, 2, 10, 3, 11);
+      second = __builtin_shufflevector(x.a, x.b, 4, 12, 5, 13, 6, 14, 7, 15);
+    }
+    *reinterpret_cast<V8*>(out + h * kv.dim + a) = first;
+    *reinterpret_cast<V8*>(out + h * kv.dim + b) = second;
   }
 }
 
@@ -542,13 +714,24 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
 }
 
 // ---------------------------------------------------------------------------
-// Reading back: one workgroup per touched block and kv head, an element a thread.
+// Reading back: one workgroup per touched block and kv head, in the units of
+// the append.  K: 16 elements of a token, 32 or 64 bytes of output a thread.
+// V: 16 bytes of the page, turned across four lanes into 4 elements of a token.
+
+template <typename T, int CODE>
+__device__ __forceinline__ void put_values4(T* p, uint32_t w, float unit) {
+  T y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = (T)(Code<CODE>::value((w >> (8 * j)) & 0xFF) * unit);
+  if (sizeof(T) == 2) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(y);
+  else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(y);
+}
 
 template <typename T, int CODE>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRead R) {
   using C = Code<CODE>;
   const KvView& kv = R.kv;
-  const int dim = kv.dim;
+  const int dim = kv.dim, tid = threadIdx.x, lane = tid & 63;
   const KvBlock blk = R.blocks[blockIdx.x / kv.n_kv];
   const int head = blockIdx.x % kv.n_kv;
   const KvSeq sq = R.seqs[blk.s];
@@ -557,10 +740,37 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRead R) {
   const uint8_t* vbase = kbase + (int64_t)kv.block * dim;
   const float uk = kv.range[2 * (int64_t)page] / C::kTop, uv = kv.range[2 * (int64_t)page + 1] / C::kTop;
   const int64_t row0 = (int64_t)sq.row0 + blk.block * kv.block - sq.start;
-  for (int u = threadIdx.x; u < (blk.slot1 - blk.slot0) * dim; u += kThreads) {
-    const int slot = blk.slot0 + u / dim, d = u % dim;
-    if (R.k) ((T*)R.k)[(row0 + slot) * R.k_stride + (int64_t)head * dim + d] = (T)(C::value(kbase[kv_k_byte(slot, d, dim)]) * uk);
-    if (R.v) ((T*)R.v)[(row0 + slot) * R.v_stride + (int64_t)head * dim + d] = (T)(C::value(vbase[kv_v_byte(slot, d, dim)]) * uv);
+  const int ush = 27 - __clz(dim);
+  if (R.k) {
+    T* out = (T*)R.k + (int64_t)head * dim;
+    for (int u = tid; u < (blk.slot1 - blk.slot0) << ush; u += kThreads) {
+      const int slot = blk.slot0 + (u >> ush), d = (u & ((1 << ush) - 1)) * 16;
+      const uint4 w = ld16(kbase + kv_k_byte(slot, d, dim));
+      T* p = out + (row0 + slot) * R.k_stride + d;
+      put_values4<T, CODE>(p, w.x, uk);
+      put_values4<T, CODE>(p + 4, w.y, uk);
+      put_values4<T, CODE>(p + 8, w.z, uk);
+      put_values4<T, CODE>(p + 12, w.w, uk);
+    }
+  }
+  if (R.v) {
+    T* out = (T*)R.v + (int64_t)head * dim;
+    const int g = lane >> 4, quad = (lane >> 2) & 3, k4 = lane & 3;
+    const int group0 = blk.slot0 >> 5, group1 = (blk.slot1 + 31) >> 5;
+    for (int u = tid; u < (group1 - group0) * dim * 2; u += kThreads) {     // a multiple of 64: whole waves
+      const int group = group0 + u / (dim * 2), e = u % (dim * 2) >> 6;
+      const uint4 w = ld16(vbase + (int64_t)group * 32 * dim + e * 1024 + lane * 16);
+      const uint32_t t[4] = {quad_transpose(w.x, lane), quad_transpose(w.y, lane), quad_transpose(w.z, lane),
+                             quad_transpose(w.w, lane)};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int slot = group * 32 + h * 16 + g * 4 + k4;
+        if (slot < blk.slot0 || slot >= blk.slot1) continue;
+        T* p = out + (row0 + slot) * R.v_stride + e * 32 + quad * 4;
+        put_values4<T, CODE>(p, t[h], uv);
+        put_values4<T, CODE>(p + 16, t[2 + h], uv);
+      }
+    }
   }
 }
 
@@ -607,8 +817,11 @@ static const void* combine_of(int dim) {
 }
 
 hipError_t launch_kv_append(const KvAppend& A, hipStream_t stream) {
-  int64_t blocks = (int64_t)A.n_blocks * A.kv.n_kv;
-  if (A.q) blocks += ((int64_t)A.n_rows * A.kv.n_heads * (A.kv.dim / 16) + kThreads - 1) / kThreads;
+  int64_t blocks = ((int64_t)A.n_small * A.kv.n_kv + 3) / 4 + (int64_t)(A.n_blocks - A.n_small) * A.kv.n_kv;
+  if (A.q) {
+    const int64_t chunks = (A.kv.n_heads + A.q_heads - 1) / A.q_heads;
+    blocks += ((int64_t)A.n_rows * chunks * (A.kv.dim / 16) + kThreads - 1) / kThreads;
+  }
   return run(A.kv.dtype == SLORA_F16 ? append_of<_Float16>(A.kv.code) : append_of<float>(A.kv.code), blocks, A, stream);
 }
 

@@ -109,7 +109,7 @@ struct slora_kv_step {
   std::vector<int32_t> row_pos;
   std::vector<KvTile> tiles, combine;
   std::vector<KvPatch> patches;
-  int32_t n_rows = 0, max_len = 0;
+  int32_t n_rows = 0, max_len = 0, n_small = 0;
   int64_t n_new_pages = 0, n_parts = 0;
   const char* dev = nullptr;
 
@@ -309,6 +309,9 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
         st->blocks.push_back({i, b, std::max(0, start - b * kv->block), (int32_t)std::min<int64_t>(kv->block, end - (int64_t)b * kv->block)});
       row0 += counts[i];
     }
+    st->n_small = (int32_t)(std::stable_partition(st->blocks.begin(), st->blocks.end(), [](const KvBlock& b) {
+                              return b.slot1 - b.slot0 <= kKvSmall;
+                            }) - st->blocks.begin());
     build_tiles(st);
     // every workgroup index of a launch is 31 bits
     const int64_t most = std::max({(int64_t)st->blocks.size(), (int64_t)st->tiles.size(), st->n_parts}) * kv->d.n_kv_heads +
@@ -438,7 +441,11 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* st, int32_t laye
   A.seqs = reinterpret_cast<const KvSeq*>(st->dev);
   A.blocks = reinterpret_cast<const KvBlock*>(st->dev + st->blocks_off());
   A.n_blocks = (int32_t)st->blocks.size();
+  A.n_small = st->n_small;
   A.n_rows = st->n_rows;
+  // enough threads for about eight waves a SIMD; beyond that, more heads a thread
+  const int64_t units = (int64_t)st->n_rows * kv->d.n_heads * kv->d.head_dim / 16;
+  A.q_heads = (int32_t)std::min<int64_t>(8, std::max<int64_t>(1, units / (1 << 19)));
   A.layer = layer;
   A.q = q;
   A.q_out = q_out;
