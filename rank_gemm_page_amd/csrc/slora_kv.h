@@ -18,7 +18,7 @@ constexpr int kKvSmall = 8;       // a block that gains at most this many tokens
 // every lane reads 16 contiguous bytes and a wave 1 KiB.
 //  K: per 16 tokens and 64 elements of the head, 16 rows (tokens) of 64 bytes.
 //  V: per 32 tokens and 32 elements, 64 lanes of 16 bytes; lane (g, i) = 16 g + i
-//     holds, for elements i and 16 + i, the 8 tokens 4g .. 4g+3 and
+//     holds, for elements 2i and 2i + 1, the 8 tokens 4g .. 4g+3 and
 //     16 + 4g .. 16 + 4g+3: the tokens whose softmax weights lane (g, *) holds
 //     after the K product, which therefore feed the V product from registers.
 inline constexpr int64_t kv_k_byte(int slot, int d, int dim) {
@@ -26,8 +26,8 @@ inline constexpr int64_t kv_k_byte(int slot, int d, int dim) {
 }
 inline constexpr int64_t kv_v_byte(int slot, int d, int dim) {
   const int t = slot & 31;
-  return (int64_t)(slot >> 5) * 32 * dim + (d >> 5) * 1024 + ((t & 15) >> 2) * 256 + (d & 15) * 16 +
-         ((d >> 4) & 1) * 8 + (t >> 4) * 4 + (t & 3);
+  return (int64_t)(slot >> 5) * 32 * dim + (d >> 5) * 1024 + ((t & 15) >> 2) * 256 + ((d & 31) >> 1) * 16 +
+         (d & 1) * 8 + (t >> 4) * 4 + (t & 3);
 }
 
 struct KvView {
@@ -40,7 +40,7 @@ struct KvView {
 
 // Records of a step (device metadata, int32 words).
 struct KvSeq { int32_t seq, start, rows, row0; };            // sequence id, first position, rows, first batch row
-struct KvBlock { int32_t s, block, slot0, slot1; };          // KvSeq index, block, its slots [slot0, slot1) among the rows
+struct KvBlock { int32_t seq, block, slot0, slot1, row, pad[3]; };   // sequence id, block, its slots [slot0, slot1) among the rows, batch row of slot0
 struct KvTile { int32_t s, tile, split, splits, part, pad[3]; };   // rows tile*16.. of the sequence's packed rows; part: see below
 struct KvPatch { uint32_t lo, hi; int32_t page, pad; };      // page table entry (hi:lo) = page
 
@@ -51,7 +51,6 @@ constexpr int64_t kv_part_floats(int dim) { return (int64_t)kKvRows * (dim + 2);
 
 struct KvAppend {
   KvView kv;
-  const KvSeq* seqs;
   const KvBlock* blocks;      // n_small blocks that gain few tokens, then the others
   int32_t n_blocks, n_small, n_rows, layer;
   int32_t q_heads;            // heads a thread rotates
@@ -74,7 +73,6 @@ struct KvAttend {
 
 struct KvRead {
   KvView kv;
-  const KvSeq* seqs;
   const KvBlock* blocks;
   int32_t n_blocks, layer;
   void* k; void* v;

@@ -93,17 +93,11 @@ __global__ __launch_bounds__(kThreads) void kv_patch_kernel(int32_t* table, cons
 }
 
 // ---------------------------------------------------------------------------
-// Elements in memory, 8 or 4 at a time.
+// Elements in memory, 8 at a time.
 
 template <typename T> struct Vec;
-template <> struct Vec<_Float16> {
-  typedef half8 v8;
-  typedef _Float16 v4 __attribute__((ext_vector_type(4)));
-};
-template <> struct Vec<float> {
-  typedef float8v v8;
-  typedef float4v v4;
-};
+template <> struct Vec<_Float16> { typedef half8 v8; };
+template <> struct Vec<float> { typedef float8v v8; };
 
 // A 64-bit number rounded once.  fp16: to fp32 with the last bit set where
 // that was inexact (rounding to odd), which the rounding to fp16 then sees.
@@ -155,15 +149,16 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t x, int lane) {
 }
 
 // ---------------------------------------------------------------------------
-// Append.  An item is one touched block of one kv head.  Blocks that gain few
-// tokens are a wave's work, the others a workgroup's.
+// Append.  An item is the keys or the values of one touched block of one kv
+// head.  Blocks that gain few tokens are a wave's work, the others a
+// workgroup's.
 //
 // Keys go in units of 8 pairs of a token; values in the page's 16-byte units (2
-// elements of 8 tokens), read token by token, 4 elements a lane, and turned by
+// elements of 8 tokens), read token by token, 8 elements a lane, and turned by
 // byte transposes across four lanes.  The first pass finds the largest
-// magnitudes and keeps one unit of each a thread in registers (all there is
-// where a page holds 8 KiB); what is beyond them is read again by the second
-// pass, which writes the codes.
+// magnitude and keeps one unit a thread in registers (all there is where a page
+// holds 8 KiB); what is beyond it is read again by the second pass, which
+// writes the codes.
 
 // Bit patterns of non-negative floats order as integers, with infinities and
 // NaN above every finite one.
@@ -194,42 +189,52 @@ __device__ __forceinline__ uint4 again16(uint4 o, double ratio) {
   return make_uint4(again4<CODE>(o.x, ratio), again4<CODE>(o.y, ratio), again4<CODE>(o.z, ratio), again4<CODE>(o.w, ratio));
 }
 
-// Elements of a value unit as they are read: [8-token half][16-element half].
-template <typename T> struct Values { typename Vec<T>::v4 x[2][2]; };
+// Elements of a value unit as they are read: 8 of each of two tokens.  old: the unit as the page holds it, where the append leaves some of its
+// tokens as they are.
+template <typename T> struct Values { typename Vec<T>::v8 x[2]; uint4 old; };
+
+// What both kinds of item need.
+struct Item {
+  KvBlock blk;
+  int head, dim, ush, pos0;     // ush: log2 of the units of a token (dim / 16); pos0: position of slot 0
+  int64_t row0;                 // batch row of slot 0 (negative before the first new slot)
+  uint8_t* page;
+  float* range;
+};
+__device__ __forceinline__ Item item_of(const KvAppend& A, uint32_t at) {
+  const KvView& kv = A.kv;
+  Item it;
+  const uint32_t b = at / (uint32_t)kv.n_kv;
+  it.blk = A.blocks[b];
+  it.head = (int)(at - b * kv.n_kv);
+  it.dim = kv.dim;
+  it.ush = 27 - __clz(kv.dim);
+  it.pos0 = it.blk.block * kv.block;
+  it.row0 = (int64_t)it.blk.row - it.blk.slot0;
+  const int32_t page = kv_row(kv, it.blk.seq, A.layer, it.head)[it.blk.block];
+  it.page = (uint8_t*)kv.base + (int64_t)page * kv.page_bytes;
+  it.range = kv.range + 2 * (int64_t)page;
+  return it;
+}
 
 template <typename T, int CODE, int NT>
-__device__ __forceinline__ void store_item(const KvAppend& A, int64_t item, int tid, uint32_t* lds) {
+__device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int tid, uint32_t* lds) {
   using C = Code<CODE>;
-  typedef typename Vec<T>::v4 V4;
   const KvView& kv = A.kv;
-  const int dim = kv.dim, lane = tid & 63;
-  const KvBlock blk = A.blocks[item / kv.n_kv];
-  const int head = (int)(item % kv.n_kv);
-  const KvSeq sq = A.seqs[blk.s];
-  const int32_t page = kv_row(kv, sq.seq, A.layer, head)[blk.block];
-  uint8_t* kbase = (uint8_t*)kv.base + (int64_t)page * kv.page_bytes;
-  uint8_t* vbase = kbase + (int64_t)kv.block * dim;
-  float* range = kv.range + 2 * (int64_t)page;
-  const int pos0 = blk.block * kv.block;                       // position of slot 0
-  const int64_t row0 = (int64_t)sq.row0 + pos0 - sq.start;     // batch row of slot 0 (negative before the first new slot)
-  const T* kin = (const T*)A.k + (int64_t)head * dim;
-  const T* vin = (const T*)A.v + (int64_t)head * dim;
-  const int ush = 27 - __clz(dim);                             // log2 of the units of a token (dim / 16)
-  const int units_k = (blk.slot1 - blk.slot0) << ush;
-  const int group0 = blk.slot0 >> 5, group1 = (blk.slot1 + 31) >> 5;
-  const int units_v = (group1 - group0) << (ush + 5);          // a multiple of 64: a wave's lanes act alike
-  const int g = lane >> 4, quad = (lane >> 2) & 3, k4 = lane & 3;
-  const uint32_t held_k = blk.slot0 ? __float_as_uint(range[0]) & 0x7FFFFFFFu : 0;
-  const uint32_t held_v = blk.slot0 ? __float_as_uint(range[1]) & 0x7FFFFFFFu : 0;
+  const Item it = item_of(A, at);
+  const KvBlock& blk = it.blk;
+  const int ush = it.ush, units = (blk.slot1 - blk.slot0) << ush;
+  const T* in = (const T*)A.k + (int64_t)it.head * it.dim;
+  const uint32_t held = blk.slot0 ? __float_as_uint(it.range[0]) & 0x7FFFFFFFu : 0;
 
-  auto key = [&](int u, Pairs<T>* x, Turn* t) {
+  auto load = [&](int u, Pairs<T>* x, Turn* t) {
     const int slot = blk.slot0 + (u >> ush), c = u & ((1 << ush) - 1);
     int a, b;
     unit_runs(kv, c, &a, &b);
-    *x = load_pairs(kv, kin + (row0 + slot) * A.k_stride, a, b);
-    *t = load_turn(kv, A.cos_sin, pos0 + slot, c);
+    *x = load_pairs(kv, in + (it.row0 + slot) * A.k_stride, a, b);
+    *t = load_turn(kv, A.cos_sin, it.pos0 + slot, c);
   };
-  auto key_max = [&](const Pairs<T>& x, const Turn& t) {
+  auto largest = [&](const Pairs<T>& x, const Turn& t) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -239,56 +244,22 @@ __device__ __forceinline__ void store_item(const KvAppend& A, int64_t item, int 
     }
     return m;
   };
-  auto value = [&](int u, Values<T>* x) {
-    const int group = group0 + (u >> (ush + 5)), e = (u >> 6) & ((1 << (ush - 1)) - 1);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int slot = group * 32 + h * 16 + g * 4 + k4;
-      x->x[h][0] = x->x[h][1] = V4{};
-      if (slot >= blk.slot0 && slot < blk.slot1) {
-        const T* row = vin + (row0 + slot) * A.v_stride + e * 32 + quad * 4;
-        x->x[h][0] = *reinterpret_cast<const V4*>(row);
-        x->x[h][1] = *reinterpret_cast<const V4*>(row + 16);
-      }
-    }
-  };
-  auto value_max = [&](const Values<T>& x) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int n = 0; n < 16; ++n) m = max(m, magnitude((float)x.x[n >> 3][(n >> 2) & 1][n & 3]));
-    return m;
-  };
-
-  Pairs<T> kx{};
-  Turn kt{};
-  Values<T> vx{};
-  if (tid < units_v) value(tid, &vx);
-  if (tid < units_k) key(tid, &kx, &kt);
-  uint32_t mk = key_max(kx, kt), mv = value_max(vx);
-  for (int u = tid + NT; u < units_k; u += NT) {
+  Pairs<T> kept{};
+  Turn kept_turn{};
+  if (tid < units) load(tid, &kept, &kept_turn);
+  uint32_t m = largest(kept, kept_turn);
+  for (int u = tid + NT; u < units; u += NT) {
     Pairs<T> x;
     Turn t;
-    key(u, &x, &t);
-    mk = max(mk, key_max(x, t));
+    load(u, &x, &t);
+    m = max(m, largest(x, t));
   }
-  for (int u = tid + NT; u < units_v; u += NT) {
-    Values<T> x;
-    value(u, &x);
-    mv = max(mv, value_max(x));
-  }
-  mk = max(team_max<NT>(mk, lds), held_k);
-  mv = max(team_max<NT>(mv, lds + NT / 64), held_v);
-  const bool bad_k = mk >= 0x7F800000u, bad_v = mv >= 0x7F800000u;
-  if (tid == 0) {
-    range[0] = bad_k ? __uint_as_float(0x7FC00000u) : __uint_as_float(mk);
-    range[1] = bad_v ? __uint_as_float(0x7FC00000u) : __uint_as_float(mv);
-  }
-  const double new_k = __uint_as_float(mk), new_v = __uint_as_float(mv);
-  const double inv_k = mk ? (double)C::kTop / new_k : 0., inv_v = mv ? (double)C::kTop / new_v : 0.;
-  constexpr uint32_t kZero4 = C::kZero * 0x01010101u;
+  m = max(team_max<NT>(m, lds), held);
+  const bool bad = m >= 0x7F800000u;
+  if (tid == 0) it.range[0] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m);
+  const double grown = __uint_as_float(m), inv = m ? (double)C::kTop / grown : 0.;
 
-  // keys
-  auto put_key = [&](int u, const Pairs<T>& x, const Turn& t) {
+  auto put = [&](int u, const Pairs<T>& x, const Turn& t) {
     const int slot = blk.slot0 + (u >> ush), c = u & ((1 << ush) - 1);
     int a, b;
     unit_runs(kv, c, &a, &b);
@@ -297,38 +268,83 @@ __device__ __forceinline__ void store_item(const KvAppend& A, int64_t item, int 
     for (int j = 0; j < 8; ++j) {
       double ra, rb;
       turned((float)x.a[j], (float)x.b[j], t.c[j], t.s[j], &ra, &rb);
-      wa[j >> 2] |= C::nearest(ra * inv_k) << (8 * (j & 3));
-      wb[j >> 2] |= C::nearest(rb * inv_k) << (8 * (j & 3));
+      wa[j >> 2] |= C::nearest(ra * inv) << (8 * (j & 3));
+      wb[j >> 2] |= C::nearest(rb * inv) << (8 * (j & 3));
     }
     uint2 first = make_uint2(wa[0], wa[1]), second = make_uint2(wb[0], wb[1]);
     if (kv.pairs == SLORA_KV_NEIGHBOURS) {
       first = make_uint2(__builtin_amdgcn_perm(wb[0], wa[0], 0x05010400u), __builtin_amdgcn_perm(wb[0], wa[0], 0x07030602u));
       second = make_uint2(__builtin_amdgcn_perm(wb[1], wa[1], 0x05010400u), __builtin_amdgcn_perm(wb[1], wa[1], 0x07030602u));
     }
-    if (bad_k) first = second = make_uint2(kZero4, kZero4);
-    *reinterpret_cast<uint2*>(kbase + kv_k_byte(slot, a, dim)) = first;
-    *reinterpret_cast<uint2*>(kbase + kv_k_byte(slot, b, dim)) = second;
+    if (bad) first = second = make_uint2(C::kZero * 0x01010101u, C::kZero * 0x01010101u);
+    *reinterpret_cast<uint2*>(it.page + kv_k_byte(slot, a, it.dim)) = first;
+    *reinterpret_cast<uint2*>(it.page + kv_k_byte(slot, b, it.dim)) = second;
   };
-  if (tid < units_k) put_key(tid, kx, kt);
-  for (int u = tid + NT; u < units_k; u += NT) {
+  if (tid < units) put(tid, kept, kept_turn);
+  for (int u = tid + NT; u < units; u += NT) {
     Pairs<T> x;
     Turn t;
-    key(u, &x, &t);
-    put_key(u, x, t);
+    load(u, &x, &t);
+    put(u, x, t);
   }
-  if (blk.slot0 && mk != held_k) {                             // the range grew: older keys are coded again
-    const double ratio = bad_k ? 0. : (double)__uint_as_float(held_k) / new_k;
+  if (blk.slot0 && m != held) {                                // the range grew: older keys are coded again
+    const double ratio = bad ? 0. : (double)__uint_as_float(held) / grown;
     for (int u = tid; u < blk.slot0 << ush; u += NT) {
-      uint8_t* at = kbase + kv_k_byte(u >> ush, (u & ((1 << ush) - 1)) * 16, dim);
-      st16(at, again16<CODE>(ld16(at), ratio));
+      uint8_t* p = it.page + kv_k_byte(u >> ush, (u & ((1 << ush) - 1)) * 16, it.dim);
+      st16(p, again16<CODE>(ld16(p), ratio));
     }
   }
+}
 
-  // values
-  const bool grew = blk.slot0 && mv != held_v;
-  const double ratio = grew && !bad_v ? (double)__uint_as_float(held_v) / new_v : 0.;
-  auto put_value = [&](int u, const Values<T>& x) {
+template <typename T, int CODE, int NT>
+__device__ __forceinline__ void store_values(const KvAppend& A, uint32_t at, int tid, uint32_t* lds) {
+  using C = Code<CODE>;
+  typedef typename Vec<T>::v8 V8;
+  const KvView& kv = A.kv;
+  const Item it = item_of(A, at);
+  const KvBlock& blk = it.blk;
+  const int ush = it.ush, lane = tid & 63;
+  const int group0 = blk.slot0 >> 5, group1 = (blk.slot1 + 31) >> 5;
+  const int units = (group1 - group0) << (ush + 5);            // a multiple of 64: a wave's lanes act alike
+  const int g = lane >> 4, quad = (lane >> 2) & 3, k4 = lane & 3;
+  uint8_t* base = it.page + (int64_t)kv.block * it.dim;
+  const T* in = (const T*)A.v + (int64_t)it.head * it.dim + quad * 8;
+  const uint32_t held = blk.slot0 ? __float_as_uint(it.range[1]) & 0x7FFFFFFFu : 0;
+
+  auto load = [&](int u, Values<T>* x) {
     const int group = group0 + (u >> (ush + 5)), e = (u >> 6) & ((1 << (ush - 1)) - 1);
+    x->old = make_uint4(0, 0, 0, 0);
+    if (group * 32 < blk.slot0 || group * 32 + 32 > blk.slot1) x->old = ld16(base + (int64_t)(group0 * it.dim * 2 + u) * 16);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int slot = group * 32 + h * 16 + g * 4 + k4;
+      x->x[h] = V8{};
+      if (slot >= blk.slot0 && slot < blk.slot1)
+        x->x[h] = *reinterpret_cast<const V8*>(in + (it.row0 + slot) * A.v_stride + e * 32);
+    }
+  };
+  auto largest = [&](const Values<T>& x) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int n = 0; n < 16; ++n) m = max(m, magnitude((float)x.x[n >> 3][n & 7]));
+    return m;
+  };
+  Values<T> kept{};
+  if (tid < units) load(tid, &kept);
+  uint32_t m = largest(kept);
+  for (int u = tid + NT; u < units; u += NT) {
+    Values<T> x;
+    load(u, &x);
+    m = max(m, largest(x));
+  }
+  m = max(team_max<NT>(m, lds), held);
+  const bool bad = m >= 0x7F800000u, grew = blk.slot0 && m != held;
+  if (tid == 0) it.range[1] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m);
+  const double grown = __uint_as_float(m), inv = m ? (double)C::kTop / grown : 0.;
+  const double ratio = grew && !bad ? (double)__uint_as_float(held) / grown : 0.;
+
+  auto put = [&](int u, const Values<T>& x) {
+    const int group = group0 + (u >> (ush + 5));
     uint32_t w[4], mask[2] = {0, 0};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -341,58 +357,60 @@ __device__ __forceinline__ void store_item(const KvAppend& A, int64_t item, int 
       for (int d = 0; d < 2; ++d) {
         uint32_t c = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c |= C::nearest((double)(float)x.x[h][d][j] * inv_v) << (8 * j);
-        w[2 * d + h] = quad_transpose(bad_v ? kZero4 : c, lane);
+        for (int j = 0; j < 4; ++j) c |= C::nearest((double)(float)x.x[h][2 * j + d] * inv) << (8 * j);
+        w[2 * d + h] = quad_transpose(bad ? C::kZero * 0x01010101u : c, lane);
       }
     }
-    uint8_t* at = vbase + ((int64_t)group << (ush + 9)) + e * 1024 + lane * 16;
     if ((mask[0] & mask[1]) != 0xFFFFFFFFu) {
       if (!(mask[0] | mask[1]) && !grew) return;
-      uint4 old = ld16(at);
-      if (grew) old = again16<CODE>(old, ratio);
+      const uint4 old = grew ? again16<CODE>(x.old, ratio) : x.old;
       w[0] = (w[0] & mask[0]) | (old.x & ~mask[0]);
       w[1] = (w[1] & mask[1]) | (old.y & ~mask[1]);
       w[2] = (w[2] & mask[0]) | (old.z & ~mask[0]);
       w[3] = (w[3] & mask[1]) | (old.w & ~mask[1]);
     }
-    st16(at, make_uint4(w[0], w[1], w[2], w[3]));
+    st16(base + (int64_t)(group0 * it.dim * 2 + u) * 16, make_uint4(w[0], w[1], w[2], w[3]));
   };
-  if (tid < units_v) put_value(tid, vx);
-  for (int u = tid + NT; u < units_v; u += NT) {
+  if (tid < units) put(tid, kept);
+  for (int u = tid + NT; u < units; u += NT) {
     Values<T> x;
-    value(u, &x);
-    put_value(u, x);
+    load(u, &x);
+    put(u, x);
   }
-  if (grew)
-    for (int u = tid; u < group0 << (ush + 5); u += NT) {
-      uint8_t* at = vbase + (int64_t)u * 16;
-      st16(at, again16<CODE>(ld16(at), ratio));
-    }
+  if (grew)                                                    // groups of older values only
+    for (int u = tid; u < group0 << (ush + 5); u += NT)
+      st16(base + (int64_t)u * 16, again16<CODE>(ld16(base + (int64_t)u * 16), ratio));
 }
 
-// Workgroups: items a wave each (A.n_small blocks), items a workgroup each,
-// then q: a thread rotates one unit of A.q_heads heads of a row, so that a
-// row's angles are read once for them.
+// Workgroups: the small blocks' items (keys, then values of a block's heads), a
+// wave each; the others', a workgroup each; then q: a thread rotates one unit
+// of A.q_heads heads of a row, so that a row's angles are read once for them.
 template <typename T, int CODE>
-__global__ __launch_bounds__(kThreads, 4) void kv_append_kernel(KvAppend A) {
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
   typedef typename Vec<T>::v8 V8;
   const KvView& kv = A.kv;
-  __shared__ uint32_t lds[2 * kThreads / 64];
+  __shared__ uint32_t lds[kThreads / 64];
   const int tid = threadIdx.x;
-  const int64_t small = (int64_t)A.n_small * kv.n_kv, small_wgs = (small + 3) / 4;
-  const int64_t wgs = small_wgs + (int64_t)(A.n_blocks - A.n_small) * kv.n_kv;
+  const uint32_t small = (uint32_t)A.n_small * kv.n_kv, small_wgs = (small + 1) / 2;
+  const uint32_t wgs = small_wgs + 2 * (uint32_t)(A.n_blocks - A.n_small) * kv.n_kv;
   if (blockIdx.x < small_wgs) {
-    const int64_t item = (int64_t)blockIdx.x * 4 + (tid >> 6);
-    if (item < small) store_item<T, CODE, 64>(A, item, tid & 63, nullptr);
+    const uint32_t wave = uni(tid >> 6), item = blockIdx.x * 2 + (wave >> 1);
+    if (item >= small) return;
+    if (wave & 1) store_values<T, CODE, 64>(A, item, tid & 63, nullptr);
+    else store_keys<T, CODE, 64>(A, item, tid & 63, nullptr);
     return;
   }
   if (blockIdx.x < wgs) {
-    store_item<T, CODE, kThreads>(A, small + blockIdx.x - small_wgs, tid, lds);
+    const uint32_t item = blockIdx.x - small_wgs;
+    if (item & 1) store_values<T, CODE, kThreads>(A, small + (item >> 1), tid, lds);
+    else store_keys<T, CODE, kThreads>(A, small + (item >> 1), tid, lds);
     return;
   }
-  const int per = kv.dim / 16, chunks = (kv.n_heads + A.q_heads - 1) / A.q_heads;
-  const int64_t i = (blockIdx.x - wgs) * kThreads + tid, rc = i / per;
-  const int u = (int)(i - rc * per), row = (int)(rc / chunks), h0 = (int)(rc - (int64_t)row * chunks) * A.q_heads;
+  const uint32_t chunks = (kv.n_heads + A.q_heads - 1) / A.q_heads;
+  const int ush = 27 - __clz(kv.dim);
+  const uint64_t i = (uint64_t)(blockIdx.x - wgs) * kThreads + tid;
+  const uint32_t rc = (uint32_t)(i >> ush);
+  const int u = (int)(i & ((1u << ush) - 1)), row = (int)(rc / chunks), h0 = (int)(rc - row * chunks) * A.q_heads;
   if (row >= A.n_rows) return;
   int a, b;
   unit_runs(kv, u, &a, &b);
@@ -401,6 +419,7 @@ __global__ __launch_bounds__(kThreads, 4) void kv_append_kernel(KvAppend A) {
   const T* in = (const T*)A.q + row * A.q_stride;
   T* out = (T*)A.q_out + row * A.q_out_stride;
   const int h1 = min(kv.n_heads, h0 + A.q_heads);
+#pragma unroll 4
   for (int h = h0; h < h1; ++h) {
     Pairs<T> x = load_pairs(kv, in + h * kv.dim, a, b);
     if (turns) {
@@ -647,7 +666,11 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
   for (int c0 = 0; c0 < D; c0 += DC) {
     if (c0) __syncthreads();
 #pragma unroll
-    for (int n = 0; n < DC / 16; ++n) *(float4v*)&lds_o[wave][i][n * 16 + g * 4] = acc[c0 / 16 + n];
+    for (int e = 0; e < DC / 32; ++e) {
+      const float4v a = acc[c0 / 16 + 2 * e], b = acc[c0 / 16 + 2 * e + 1];
+      *(float4v*)&lds_o[wave][i][e * 32 + g * 8] = float4v{a[0], b[0], a[1], b[1]};
+      *(float4v*)&lds_o[wave][i][e * 32 + g * 8 + 4] = float4v{a[2], b[2], a[3], b[3]};
+    }
     __syncthreads();
     float mm = lds_ml[0][orow][0];
 #pragma unroll
@@ -714,17 +737,20 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
 }
 
 // ---------------------------------------------------------------------------
-// Reading back: one workgroup per touched block and kv head, in the units of
-// the append.  K: 16 elements of a token, 32 or 64 bytes of output a thread.
-// V: 16 bytes of the page, turned across four lanes into 4 elements of a token.
+// Reading back: one workgroup per touched block and kv head.  A thread takes 8
+// elements of a token from K, and a 16-byte unit of V, turned across four lanes
+// into 8 elements of each of two tokens, so that stores are 16 bytes a lane and
+// 64 bytes or more a run.
 
 template <typename T, int CODE>
-__device__ __forceinline__ void put_values4(T* p, uint32_t w, float unit) {
-  T y[4];
+__device__ __forceinline__ void put8(T* p, uint32_t a, uint32_t b, float unit) {
+  typename Vec<T>::v8 y;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) y[j] = (T)(Code<CODE>::value((w >> (8 * j)) & 0xFF) * unit);
-  if (sizeof(T) == 2) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(y);
-  else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(y);
+  for (int j = 0; j < 4; ++j) {
+    y[j] = (T)(Code<CODE>::value((a >> (8 * j)) & 0xFF) * unit);
+    y[4 + j] = (T)(Code<CODE>::value((b >> (8 * j)) & 0xFF) * unit);
+  }
+  *reinterpret_cast<typename Vec<T>::v8*>(p) = y;
 }
 
 template <typename T, int CODE>
@@ -734,41 +760,58 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRead R) {
   const int dim = kv.dim, tid = threadIdx.x, lane = tid & 63;
   const KvBlock blk = R.blocks[blockIdx.x / kv.n_kv];
   const int head = blockIdx.x % kv.n_kv;
-  const KvSeq sq = R.seqs[blk.s];
-  const int32_t page = kv_row(kv, sq.seq, R.layer, head)[blk.block];
+  const int32_t page = kv_row(kv, blk.seq, R.layer, head)[blk.block];
   const uint8_t* kbase = (const uint8_t*)kv.base + (int64_t)page * kv.page_bytes;
   const uint8_t* vbase = kbase + (int64_t)kv.block * dim;
-  const float uk = kv.range[2 * (int64_t)page] / C::kTop, uv = kv.range[2 * (int64_t)page + 1] / C::kTop;
-  const int64_t row0 = (int64_t)sq.row0 + blk.block * kv.block - sq.start;
-  const int ush = 27 - __clz(dim);
-  if (R.k) {
-    T* out = (T*)R.k + (int64_t)head * dim;
-    for (int u = tid; u < (blk.slot1 - blk.slot0) << ush; u += kThreads) {
-      const int slot = blk.slot0 + (u >> ush), d = (u & ((1 << ush) - 1)) * 16;
-      const uint4 w = ld16(kbase + kv_k_byte(slot, d, dim));
-      T* p = out + (row0 + slot) * R.k_stride + d;
-      put_values4<T, CODE>(p, w.x, uk);
-      put_values4<T, CODE>(p + 4, w.y, uk);
-      put_values4<T, CODE>(p + 8, w.z, uk);
-      put_values4<T, CODE>(p + 12, w.w, uk);
-    }
-  }
-  if (R.v) {
-    T* out = (T*)R.v + (int64_t)head * dim;
-    const int g = lane >> 4, quad = (lane >> 2) & 3, k4 = lane & 3;
-    const int group0 = blk.slot0 >> 5, group1 = (blk.slot1 + 31) >> 5;
-    for (int u = tid; u < (group1 - group0) * dim * 2; u += kThreads) {     // a multiple of 64: whole waves
-      const int group = group0 + u / (dim * 2), e = u % (dim * 2) >> 6;
-      const uint4 w = ld16(vbase + (int64_t)group * 32 * dim + e * 1024 + lane * 16);
-      const uint32_t t[4] = {quad_transpose(w.x, lane), quad_transpose(w.y, lane), quad_transpose(w.z, lane),
-                             quad_transpose(w.w, lane)};
+  const float* range = kv.range + 2 * (int64_t)page;
+  const int64_t row0 = (int64_t)blk.row - blk.slot0;
+  const int ush = 27 - __clz(dim), g = lane >> 4, quad = (lane >> 2) & 3, k4 = lane & 3;
+  const int group0 = blk.slot0 >> 5, group1 = (blk.slot1 + 31) >> 5;
+  const int units_k = R.k ? (blk.slot1 - blk.slot0) << (ush + 1) : 0;
+  const int units_v = R.v ? (group1 - group0) << (ush + 5) : 0;             // a multiple of 64: whole waves
+  T* kout = (T*)R.k + (int64_t)head * dim;
+  T* vout = (T*)R.v + (int64_t)head * dim;
+  // four units of K and two of V a thread at a time, all loaded before the first is used
+  for (int u0 = 0; u0 < max(units_k, 2 * units_v); u0 += 4 * kThreads) {
+    uint2 kw[4];
+    uint4 vw[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int slot = group * 32 + h * 16 + g * 4 + k4;
-        if (slot < blk.slot0 || slot >= blk.slot1) continue;
-        T* p = out + (row0 + slot) * R.v_stride + e * 32 + quad * 4;
-        put_values4<T, CODE>(p, t[h], uv);
-        put_values4<T, CODE>(p + 16, t[2 + h], uv);
+    for (int n = 0; n < 4; ++n) {
+      const int u = u0 + tid + n * kThreads;
+      if (u < units_k)
+        kw[n] = *reinterpret_cast<const uint2*>(
+            kbase + kv_k_byte(blk.slot0 + (u >> (ush + 1)), (u & ((2 << ush) - 1)) * 8, dim));
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int u = u0 / 2 + tid + n * kThreads;
+      if (u < units_v)
+        vw[n] = ld16(vbase + ((int64_t)(group0 + (u >> (ush + 5))) << (ush + 9)) +
+                     ((u >> 6) & ((1 << (ush - 1)) - 1)) * 1024 + lane * 16);
+    }
+    const float uk = range[0] / C::kTop, uv = range[1] / C::kTop;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int u = u0 + tid + n * kThreads;
+      if (u < units_k)
+        put8<T, CODE>(kout + (row0 + blk.slot0 + (u >> (ush + 1))) * R.k_stride + (u & ((2 << ush) - 1)) * 8, kw[n].x,
+                      kw[n].y, uk);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int u = u0 / 2 + tid + n * kThreads;
+      if (u < units_v) {
+        const int group = group0 + (u >> (ush + 5)), e = (u >> 6) & ((1 << (ush - 1)) - 1);
+        const uint32_t even[2] = {quad_transpose(vw[n].x, lane), quad_transpose(vw[n].y, lane)};
+        const uint32_t odd[2] = {quad_transpose(vw[n].z, lane), quad_transpose(vw[n].w, lane)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int slot = group * 32 + h * 16 + g * 4 + k4;
+          if (slot >= blk.slot0 && slot < blk.slot1)
+            put8<T, CODE>(vout + (row0 + slot) * R.v_stride + e * 32 + quad * 8,
+                          __builtin_amdgcn_perm(odd[h], even[h], 0x05010400u),
+                          __builtin_amdgcn_perm(odd[h], even[h], 0x07030602u), uv);
+        }
       }
     }
   }
@@ -817,7 +860,7 @@ static const void* combine_of(int dim) {
 }
 
 hipError_t launch_kv_append(const KvAppend& A, hipStream_t stream) {
-  int64_t blocks = ((int64_t)A.n_small * A.kv.n_kv + 3) / 4 + (int64_t)(A.n_blocks - A.n_small) * A.kv.n_kv;
+  int64_t blocks = ((int64_t)A.n_small * A.kv.n_kv + 1) / 2 + 2 * (int64_t)(A.n_blocks - A.n_small) * A.kv.n_kv;
   if (A.q) {
     const int64_t chunks = (A.kv.n_heads + A.q_heads - 1) / A.q_heads;
     blocks += ((int64_t)A.n_rows * chunks * (A.kv.dim / 16) + kThreads - 1) / kThreads;

@@ -306,7 +306,9 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
       patches += (blocks - s.entered) * kv->per_block();
       for (int32_t p = start; p < end; ++p) st->row_pos.push_back(p);
       for (int32_t b = start / kv->block; counts[i] && b < blocks; ++b)
-        st->blocks.push_back({i, b, std::max(0, start - b * kv->block), (int32_t)std::min<int64_t>(kv->block, end - (int64_t)b * kv->block)});
+        st->blocks.push_back({seqs[i], b, std::max(0, start - b * kv->block),
+                              (int32_t)std::min<int64_t>(kv->block, end - (int64_t)b * kv->block),
+                              row0 + std::max(0, b * kv->block - start), {0, 0, 0}});
       row0 += counts[i];
     }
     st->n_small = (int32_t)(std::stable_partition(st->blocks.begin(), st->blocks.end(), [](const KvBlock& b) {
@@ -314,9 +316,9 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
                             }) - st->blocks.begin());
     build_tiles(st);
     // every workgroup index of a launch is 31 bits
-    const int64_t most = std::max({(int64_t)st->blocks.size(), (int64_t)st->tiles.size(), st->n_parts}) * kv->d.n_kv_heads +
+    const int64_t most = std::max({2 * (int64_t)st->blocks.size(), (int64_t)st->tiles.size(), st->n_parts}) * kv->d.n_kv_heads +
                          rows * kv->d.n_heads * kv->d.head_dim / 16 / kThreads;
-    if (most > INT32_MAX / 2 || patches > INT32_MAX / 2) {
+    if (most > INT32_MAX / 2 || rows * kv->d.n_heads > INT32_MAX / 2 || patches > INT32_MAX / 2) {
       delete st;
       return fail(SLORA_E_INVAL, "slora_kv_build_step: the step is too large for one launch");
     }
@@ -438,7 +440,6 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* st, int32_t laye
   if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
   KvAppend A{};
   A.kv = kv->view();
-  A.seqs = reinterpret_cast<const KvSeq*>(st->dev);
   A.blocks = reinterpret_cast<const KvBlock*>(st->dev + st->blocks_off());
   A.n_blocks = (int32_t)st->blocks.size();
   A.n_small = st->n_small;
@@ -509,7 +510,6 @@ slora_status slora_kv_read(slora_kv* kv, const slora_kv_step* st, int32_t layer,
   if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
   KvRead R{};
   R.kv = kv->view();
-  R.seqs = reinterpret_cast<const KvSeq*>(st->dev);
   R.blocks = reinterpret_cast<const KvBlock*>(st->dev + st->blocks_off());
   R.n_blocks = (int32_t)st->blocks.size();
   R.layer = layer;
