@@ -11,7 +11,6 @@ namespace slora {
 
 constexpr int kKvGroup = 32;      // tokens of one attention step: block_tokens is a multiple
 constexpr int kKvRows = 16;       // query rows of one row tile
-constexpr int kKvSmall = 8;       // a block that gains at most this many tokens is one wave's append
 
 // Page layout (one block of one kv head): the K codes, then the V codes, both
 // in the order in which the 16x16x32 matrix instruction takes them, so that
@@ -51,9 +50,10 @@ constexpr int64_t kv_part_floats(int dim) { return (int64_t)kKvRows * (dim + 2);
 
 struct KvAppend {
   KvView kv;
-  const KvBlock* blocks;      // n_small blocks that gain few tokens, then the others
+  const KvBlock* blocks;      // n_small blocks that gain one token, then the others
   int32_t n_blocks, n_small, n_rows, layer;
   int32_t q_heads;            // heads a thread rotates
+  uint32_t q_share;           // workgroups of q among all, of 2^32 (set by the launch)
   const void* q; void* q_out; const void* k; const void* v;
   int64_t q_stride, q_out_stride, k_stride, v_stride;
   const float* cos_sin;

@@ -149,11 +149,10 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t x, int lane) {
 }
 
 // ---------------------------------------------------------------------------
-// Append.  An item is the keys or the values of one touched block of one kv
-// head.  Blocks that gain few tokens are a wave's work, the others a
-// workgroup's.
-//
-// Keys go in units of 8 pairs of a token; values in the page's 16-byte units (2
+// Append.  Blocks that gain one token (decode) are a wave's work, keys and
+// values together, a pair of elements of each a lane (store_one).  Otherwise an
+// item is the keys or the values of one touched block of one kv head, and a
+// workgroup's work: keys go in units of 8 pairs of a token; values in the page's 16-byte units (2
 // elements of 8 tokens), read token by token, 8 elements a lane, and turned by
 // byte transposes across four lanes.  The first pass finds the largest
 // magnitude and keeps one unit a thread in registers (all there is where a page
@@ -165,15 +164,17 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t x, int lane) {
 __device__ __forceinline__ uint32_t magnitude(double x) { return __float_as_uint(fabsf((float)x)); }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(fabsf(x)); }
 
-template <int NT>
-__device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* lds) {
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 #pragma unroll
   for (int m = 32; m; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
-  if (NT == 64) return v;
+  return v;
+}
+__device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t* lds) {
+  v = wave_max(v);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NT / 64; ++w) v = max(v, lds[w]);
+  for (int w = 0; w < kThreads / 64; ++w) v = max(v, lds[w]);
   return v;
 }
 
@@ -217,7 +218,83 @@ __device__ __forceinline__ Item item_of(const KvAppend& A, uint32_t at) {
   return it;
 }
 
-template <typename T, int CODE, int NT>
+// One token of one head by a wave: lane v takes pair v of the keys and, of the
+// values, elements 2v and 2v + 1, which are two bytes of one 16-byte unit.
+template <typename T, int CODE>
+__device__ __forceinline__ void store_one(const KvAppend& A, uint32_t at, int lane) {
+  using C = Code<CODE>;
+  constexpr int N = 2;                                         // pairs a lane: 1 up to 128 elements, 2 for 256
+  const KvView& kv = A.kv;
+  const Item it = item_of(A, at);
+  const int dim = it.dim, slot = it.blk.slot0, t = slot & 31, g = (t & 15) >> 2;
+  const int half = kv.rot >> 1, shift = 8 * (t & 3), high = t >> 4;
+  uint8_t* vbase = it.page + (int64_t)kv.block * dim;
+  const T* kin = (const T*)A.k + it.blk.row * A.k_stride + (int64_t)it.head * dim;
+  const T* vin = (const T*)A.v + it.blk.row * A.v_stride + (int64_t)it.head * dim;
+  const float* cs = A.cos_sin + (int64_t)(it.pos0 + slot) * kv.rot;
+  const uint32_t held_k = slot ? __float_as_uint(it.range[0]) & 0x7FFFFFFFu : 0;
+  const uint32_t held_v = slot ? __float_as_uint(it.range[1]) & 0x7FFFFFFFu : 0;
+  double ka[N], kb[N];
+  float v0[N], v1[N];
+  uint4 old[N];
+  int da[N], db[N];
+  uint32_t mk = 0, mv = 0;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int p = lane + 64 * n;
+    if (2 * p >= dim) continue;
+    const bool turns = p < half, split = turns && kv.pairs == SLORA_KV_HALVES;
+    da[n] = split ? p : 2 * p;
+    db[n] = split ? half + p : 2 * p + 1;
+    turned((float)kin[da[n]], (float)kin[db[n]], turns ? cs[p] : 1.f, turns ? cs[half + p] : 0.f, &ka[n], &kb[n]);
+    v0[n] = (float)vin[2 * p];
+    v1[n] = (float)vin[2 * p + 1];
+    // the unit's other tokens, of which none is there yet in the first one's case
+    old[n] = ld16(vbase + (int64_t)(slot >> 5) * 32 * dim + (p >> 4) * 1024 + g * 256 + (p & 15) * 16);
+    mk = max(mk, max(magnitude(ka[n]), magnitude(kb[n])));
+    mv = max(mv, max(magnitude(v0[n]), magnitude(v1[n])));
+  }
+  mk = max(wave_max(mk), held_k);
+  mv = max(wave_max(mv), held_v);
+  const bool bad_k = mk >= 0x7F800000u, bad_v = mv >= 0x7F800000u;
+  if (lane == 0) {
+    it.range[0] = bad_k ? __uint_as_float(0x7FC00000u) : __uint_as_float(mk);
+    it.range[1] = bad_v ? __uint_as_float(0x7FC00000u) : __uint_as_float(mv);
+  }
+  const double new_k = __uint_as_float(mk), new_v = __uint_as_float(mv);
+  const double inv_k = mk ? (double)C::kTop / new_k : 0., inv_v = mv ? (double)C::kTop / new_v : 0.;
+  const bool grew_k = slot && mk != held_k, grew_v = slot && mv != held_v;
+  const double ratio_v = grew_v && !bad_v ? (double)__uint_as_float(held_v) / new_v : 0.;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int p = lane + 64 * n;
+    if (2 * p >= dim) continue;
+    it.page[kv_k_byte(slot, da[n], dim)] = (uint8_t)(bad_k ? C::kZero : C::nearest(ka[n] * inv_k));
+    it.page[kv_k_byte(slot, db[n], dim)] = (uint8_t)(bad_k ? C::kZero : C::nearest(kb[n] * inv_k));
+    const uint32_t c0 = bad_v ? C::kZero : C::nearest((double)v0[n] * inv_v);
+    const uint32_t c1 = bad_v ? C::kZero : C::nearest((double)v1[n] * inv_v);
+    uint4 w = grew_v ? again16<CODE>(old[n], ratio_v) : old[n];
+    uint32_t& w0 = high ? w.y : w.x;
+    uint32_t& w1 = high ? w.w : w.z;
+    w0 = (w0 & ~(0xFFu << shift)) | c0 << shift;
+    w1 = (w1 & ~(0xFFu << shift)) | c1 << shift;
+    st16(vbase + (int64_t)(slot >> 5) * 32 * dim + (p >> 4) * 1024 + g * 256 + (p & 15) * 16, w);
+  }
+  if (grew_k) {
+    const double ratio = bad_k ? 0. : (double)__uint_as_float(held_k) / new_k;
+    for (int u = lane; u < slot << it.ush; u += 64) {
+      uint8_t* p = it.page + kv_k_byte(u >> it.ush, (u & ((1 << it.ush) - 1)) * 16, dim);
+      st16(p, again16<CODE>(ld16(p), ratio));
+    }
+  }
+  if (grew_v)                                                  // every unit but those the token is in
+    for (int u = lane; u < ((slot >> 5) + 1) << (it.ush + 5); u += 64) {
+      if (u >> (it.ush + 5) == slot >> 5 && ((u >> 4) & 3) == g) continue;
+      st16(vbase + (int64_t)u * 16, again16<CODE>(ld16(vbase + (int64_t)u * 16), ratio_v));
+    }
+}
+
+template <typename T, int CODE>
 __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int tid, uint32_t* lds) {
   using C = Code<CODE>;
   const KvView& kv = A.kv;
@@ -248,13 +325,13 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
   Turn kept_turn{};
   if (tid < units) load(tid, &kept, &kept_turn);
   uint32_t m = largest(kept, kept_turn);
-  for (int u = tid + NT; u < units; u += NT) {
+  for (int u = tid + kThreads; u < units; u += kThreads) {
     Pairs<T> x;
     Turn t;
     load(u, &x, &t);
     m = max(m, largest(x, t));
   }
-  m = max(team_max<NT>(m, lds), held);
+  m = max(team_max(m, lds), held);
   const bool bad = m >= 0x7F800000u;
   if (tid == 0) it.range[0] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m);
   const double grown = __uint_as_float(m), inv = m ? (double)C::kTop / grown : 0.;
@@ -281,7 +358,7 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
     *reinterpret_cast<uint2*>(it.page + kv_k_byte(slot, b, it.dim)) = second;
   };
   if (tid < units) put(tid, kept, kept_turn);
-  for (int u = tid + NT; u < units; u += NT) {
+  for (int u = tid + kThreads; u < units; u += kThreads) {
     Pairs<T> x;
     Turn t;
     load(u, &x, &t);
@@ -289,14 +366,14 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
   }
   if (blk.slot0 && m != held) {                                // the range grew: older keys are coded again
     const double ratio = bad ? 0. : (double)__uint_as_float(held) / grown;
-    for (int u = tid; u < blk.slot0 << ush; u += NT) {
+    for (int u = tid; u < blk.slot0 << ush; u += kThreads) {
       uint8_t* p = it.page + kv_k_byte(u >> ush, (u & ((1 << ush) - 1)) * 16, it.dim);
       st16(p, again16<CODE>(ld16(p), ratio));
     }
   }
 }
 
-template <typename T, int CODE, int NT>
+template <typename T, int CODE>
 __device__ __forceinline__ void store_values(const KvAppend& A, uint32_t at, int tid, uint32_t* lds) {
   using C = Code<CODE>;
   typedef typename Vec<T>::v8 V8;
@@ -332,12 +409,12 @@ __device__ __forceinline__ void store_values(const KvAppend& A, uint32_t at, int
   Values<T> kept{};
   if (tid < units) load(tid, &kept);
   uint32_t m = largest(kept);
-  for (int u = tid + NT; u < units; u += NT) {
+  for (int u = tid + kThreads; u < units; u += kThreads) {
     Values<T> x;
     load(u, &x);
     m = max(m, largest(x));
   }
-  m = max(team_max<NT>(m, lds), held);
+  m = max(team_max(m, lds), held);
   const bool bad = m >= 0x7F800000u, grew = blk.slot0 && m != held;
   if (tid == 0) it.range[1] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m);
   const double grown = __uint_as_float(m), inv = m ? (double)C::kTop / grown : 0.;
@@ -372,43 +449,44 @@ __device__ __forceinline__ void store_values(const KvAppend& A, uint32_t at, int
     st16(base + (int64_t)(group0 * it.dim * 2 + u) * 16, make_uint4(w[0], w[1], w[2], w[3]));
   };
   if (tid < units) put(tid, kept);
-  for (int u = tid + NT; u < units; u += NT) {
+  for (int u = tid + kThreads; u < units; u += kThreads) {
     Values<T> x;
     load(u, &x);
     put(u, x);
   }
   if (grew)                                                    // groups of older values only
-    for (int u = tid; u < group0 << (ush + 5); u += NT)
+    for (int u = tid; u < group0 << (ush + 5); u += kThreads)
       st16(base + (int64_t)u * 16, again16<CODE>(ld16(base + (int64_t)u * 16), ratio));
 }
 
-// Workgroups: the small blocks' items (keys, then values of a block's heads), a
-// wave each; the others', a workgroup each; then q: a thread rotates one unit
-// of A.q_heads heads of a row, so that a row's angles are read once for them.
+// Workgroups: single tokens, four (block, head) pairs each; items of the other
+// blocks; and q, whose workgroups stream and are spread evenly among those,
+// which wait: a thread rotates one unit of A.q_heads heads of a row, so that a
+// row's angles are read once for them.
 template <typename T, int CODE>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
   typedef typename Vec<T>::v8 V8;
   const KvView& kv = A.kv;
   __shared__ uint32_t lds[kThreads / 64];
   const int tid = threadIdx.x;
-  const uint32_t small = (uint32_t)A.n_small * kv.n_kv, small_wgs = (small + 1) / 2;
-  const uint32_t wgs = small_wgs + 2 * (uint32_t)(A.n_blocks - A.n_small) * kv.n_kv;
-  if (blockIdx.x < small_wgs) {
-    const uint32_t wave = uni(tid >> 6), item = blockIdx.x * 2 + (wave >> 1);
-    if (item >= small) return;
-    if (wave & 1) store_values<T, CODE, 64>(A, item, tid & 63, nullptr);
-    else store_keys<T, CODE, 64>(A, item, tid & 63, nullptr);
-    return;
-  }
-  if (blockIdx.x < wgs) {
-    const uint32_t item = blockIdx.x - small_wgs;
-    if (item & 1) store_values<T, CODE, kThreads>(A, small + (item >> 1), tid, lds);
-    else store_keys<T, CODE, kThreads>(A, small + (item >> 1), tid, lds);
+  // q workgroups up to here, and whether this is one
+  const uint32_t q_wg = __umulhi(blockIdx.x, A.q_share);
+  const bool is_q = __umulhi(blockIdx.x + 1, A.q_share) != q_wg;
+  if (!is_q) {
+    const uint32_t wg = blockIdx.x - q_wg, small = (uint32_t)A.n_small * kv.n_kv, small_wgs = (small + 3) / 4;
+    if (wg < small_wgs) {
+      const uint32_t item = uni(wg * 4 + (tid >> 6));
+      if (item < small) store_one<T, CODE>(A, item, tid & 63);
+    } else {
+      const uint32_t item = wg - small_wgs;
+      if (item & 1) store_values<T, CODE>(A, small + (item >> 1), tid, lds);
+      else store_keys<T, CODE>(A, small + (item >> 1), tid, lds);
+    }
     return;
   }
   const uint32_t chunks = (kv.n_heads + A.q_heads - 1) / A.q_heads;
   const int ush = 27 - __clz(kv.dim);
-  const uint64_t i = (uint64_t)(blockIdx.x - wgs) * kThreads + tid;
+  const uint64_t i = (uint64_t)q_wg * kThreads + tid;
   const uint32_t rc = (uint32_t)(i >> ush);
   const int u = (int)(i & ((1u << ush) - 1)), row = (int)(rc / chunks), h0 = (int)(rc - row * chunks) * A.q_heads;
   if (row >= A.n_rows) return;
@@ -859,13 +937,18 @@ static const void* combine_of(int dim) {
          : dim == 128 ? (const void*)kv_combine_kernel<T, 128> : (const void*)kv_combine_kernel<T, 256>;
 }
 
-hipError_t launch_kv_append(const KvAppend& A, hipStream_t stream) {
-  int64_t blocks = ((int64_t)A.n_small * A.kv.n_kv + 1) / 2 + 2 * (int64_t)(A.n_blocks - A.n_small) * A.kv.n_kv;
+hipError_t launch_kv_append(const KvAppend& A0, hipStream_t stream) {
+  KvAppend A = A0;
+  const int64_t items = ((int64_t)A.n_small * A.kv.n_kv + 3) / 4 + 2 * (int64_t)(A.n_blocks - A.n_small) * A.kv.n_kv;
+  int64_t q = 0;
   if (A.q) {
     const int64_t chunks = (A.kv.n_heads + A.q_heads - 1) / A.q_heads;
-    blocks += ((int64_t)A.n_rows * chunks * (A.kv.dim / 16) + kThreads - 1) / kThreads;
+    q = ((int64_t)A.n_rows * chunks * (A.kv.dim / 16) + kThreads - 1) / kThreads;
   }
-  return run(A.kv.dtype == SLORA_F16 ? append_of<_Float16>(A.kv.code) : append_of<float>(A.kv.code), blocks, A, stream);
+  // workgroup b has q workgroups floor(b * share / 2^32) before it: with the
+  // share rounded up, exactly q of all (there is always an item: q < all)
+  A.q_share = (uint32_t)((((uint64_t)q << 32) + (uint64_t)(q + items) - 1) / (uint64_t)(q + items));
+  return run(A.kv.dtype == SLORA_F16 ? append_of<_Float16>(A.kv.code) : append_of<float>(A.kv.code), q + items, A, stream);
 }
 
 hipError_t launch_kv_attend(const KvAttend& A, hipStream_t stream) {

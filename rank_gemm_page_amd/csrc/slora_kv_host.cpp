@@ -312,7 +312,7 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
       row0 += counts[i];
     }
     st->n_small = (int32_t)(std::stable_partition(st->blocks.begin(), st->blocks.end(), [](const KvBlock& b) {
-                              return b.slot1 - b.slot0 <= kKvSmall;
+                              return b.slot1 - b.slot0 == 1;
                             }) - st->blocks.begin());
     build_tiles(st);
     // every workgroup index of a launch is 31 bits
