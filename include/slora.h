@@ -503,9 +503,10 @@ const char* slora_last_error(void);
  *
  *     a_i' = a_i cos(p, i) - b_i sin(p, i)     b_i' = b_i cos(p, i) + a_i sin(p, i)
  *
- * in 64 bits, rounded once; pairs are (i, i + rot_dim/2) (SLORA_KV_HALVES) or
- * (2i, 2i + 1) (SLORA_KV_NEIGHBOURS); elements from rot_dim on stay as they
- * are.  cos_sin is the caller's table, device fp32 [n_positions][rot_dim]: a
+ * pairs are (i, i + rot_dim/2) (SLORA_KV_HALVES) or (2i, 2i + 1)
+ * (SLORA_KV_NEIGHBOURS); elements from rot_dim on stay as they are.  Keys are
+ * rotated in 64 bits before they are coded, q in fp32 (a product and the sum
+ * rounded once each) and rounded to the pool dtype.  cos_sin is the caller's table, device fp32 [n_positions][rot_dim]: a
  * position's rot_dim/2 cosines, then its rot_dim/2 sines.
  *
  * One step of a server: slora_kv_build_step names the sequences of the batch

@@ -45,6 +45,17 @@ def rotate(x, cs, rot, pairs):
     return y
 
 
+def rotation_error(x, cs, rot, pairs):
+    """Bound on fp32 rotation's error before its last rounding: one rounding of a product and one of the sum, 2^-24 of
+    at most |a c| + |b s| each."""
+    y = np.abs(rotate(np.abs(x), np.abs(cs) if rot else None, rot, pairs))
+    if rot:     # |a| |c| - |b| |s| in one half: take the other sign there
+        flipped = np.abs(cs).copy()
+        flipped[:, rot // 2:] *= -1
+        y = np.maximum(y, np.abs(rotate(np.abs(x), flipped, rot, pairs)))
+    return 2.0 ** -23 * y
+
+
 class KvModel:
     """Sequences of one cache: codes and ranges per (sequence, layer, what), what 0 = keys, 1 = values."""
 

@@ -99,17 +99,6 @@ template <typename T> struct Vec;
 template <> struct Vec<_Float16> { typedef half8 v8; };
 template <> struct Vec<float> { typedef float8v v8; };
 
-// A 64-bit number rounded once.  fp16: to fp32 with the last bit set where
-// that was inexact (rounding to odd), which the rounding to fp16 then sees.
-__device__ __forceinline__ void round_to(double r, float* y) { *y = (float)r; }
-__device__ __forceinline__ void round_to(double r, _Float16* y) {
-  const float f = (float)r;
-  const double back = (double)f;
-  uint32_t bits = __float_as_uint(f);
-  if (back != r && !(bits & 1)) bits += __builtin_fabs(back) < __builtin_fabs(r) ? 1u : ~0u;
-  *y = (_Float16)__uint_as_float(bits);
-}
-
 // Unit u of a row is eight of its pairs (a, b): of the rotated part, and behind
 // it, turned by no angle, elements 16u .. 16u + 15 as pairs of neighbours
 // (halves: of 8 and 8).  Their elements lie in two runs of 8.
@@ -138,6 +127,12 @@ __device__ __forceinline__ Turn load_turn(const KvView& kv, const float* cos_sin
 __device__ __forceinline__ void turned(float a, float b, float c, float s, double* ra, double* rb) {
   *ra = (double)a * c - (double)b * s;
   *rb = (double)b * c + (double)a * s;
+}
+
+// The same in fp32: one rounding of a product, one of the sum.
+__device__ __forceinline__ void turned(float a, float b, float c, float s, float* ra, float* rb) {
+  *ra = __builtin_fmaf(a, c, -(b * s));
+  *rb = __builtin_fmaf(b, c, a * s);
 }
 
 // 4 x 4 bytes across four lanes: lane k of a quad gets byte k of lanes 0 .. 3.
@@ -503,13 +498,10 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
     if (turns) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        double ra, rb;
+        float ra, rb;
         turned((float)x.a[j], (float)x.b[j], t.c[j], t.s[j], &ra, &rb);
-        T ya, yb;
-        round_to(ra, &ya);
-        round_to(rb, &yb);
-        x.a[j] = ya;
-        x.b[j] = yb;
+        x.a[j] = (T)ra;
+        x.b[j] = (T)rb;
       }
     }
     V8 first = x.a, second = x.b;

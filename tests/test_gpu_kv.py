@@ -30,7 +30,7 @@ def _gpu(request):
 @pytest.mark.parametrize("block,slack", [(32, 0), (96, 32)])
 def test_append_in_pieces_matches(dtype, code, dim, rot, pairs, block, slack):
     """Single tokens, pieces inside a block, over its end and over several blocks, with ranges that grow and ranges
-    that do not; rotated q bit for bit, keys and values code for code."""
+    that do not; q within its roundings, keys and values code for code."""
     block = min(block, 32 if dim == 256 else 96)        # a page of a pool holds at most 32 KiB
     with KvCase(torch, dtype, code, 6, 3, dim, block, rot, pairs, max_tokens=320, slack=slack) as c:
         for counts, gain in (([1, 3, 0], 1.0), ([1, 28, 33], 2.0), ([1, 1, 1], 0.5), ([33, 1, 64], 4.0),
@@ -148,8 +148,7 @@ def test_parts_of_one_projection_and_q_in_place(dtype):
         st, info, ws = c.step([1], [n])
         S.slora_kv_append(c.kv, st, 0, k, v, q, q, cos_sin=c.cos_sin, stream=torch.cuda.current_stream())
         c.model.append(1, 0, qkv[:, 6:9], qkv[:, 9:])
-        want = c.model.rotated(qkv[:, :6], 0).astype(c.np_dtype)
-        np.testing.assert_array_equal(q.cpu().numpy(), want)
+        c.check_rotated(q, qkv[:, :6], 0)
         np.testing.assert_array_equal(dev[:, 6:].cpu().numpy(), qkv[:, 6:])
         wide = torch.zeros((n, 10, 64), dtype=c.tdtype, device="cuda:0")
         c.attend(st, q, ws, 0.125, out=wide[:, 2:8])
