@@ -11,6 +11,7 @@ namespace slora {
 
 constexpr int kKvGroup = 32;      // tokens of one attention step: block_tokens is a multiple
 constexpr int kKvRows = 16;       // query rows of one row tile
+constexpr int kKvPromptRows = 128;   // query rows of one prompt tile
 
 // Page layout (one block of one kv head): the K codes, then the V codes, both
 // in the order in which the 16x16x32 matrix instruction takes them, so that
@@ -63,8 +64,9 @@ struct KvAppend {
 struct KvAttend {
   KvView kv;
   const KvSeq* seqs;
+  const KvTile* prompts;      // tiles of a long run of rows (fp16)
   const KvTile* tiles;        // row tiles, then (from n_tiles on) the combine entries
-  int32_t n_tiles, n_combine, layer, window;
+  int32_t n_prompts, n_tiles, n_combine, layer, window;
   const void* q; void* out;
   int64_t q_stride, out_stride;
   float scale_log2;           // scale * log2(e)

@@ -771,6 +771,227 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Attention of a long run of rows (prompts), fp16: 128 packed rows of one kv
+// head a workgroup, 32 a wave, over keys staged 64 at a time (32 for heads of
+// 256).  The codes of the next keys are loaded while these are multiplied, then
+// converted once for all four waves into fp16 in LDS, two buffers in turn.
+//
+// The 32x32x16 instruction as in the row tiles: S^T = K Q^T leaves lane (h, n) =
+// 32 h + n with query row n and keys 8a + 4h + b (a, b = 0 .. 3), registers 4a +
+// b.  Eight registers are the second operand of O^T += V^T P^T for 16 keys.  V^T
+// lies in LDS with a row's keys in that order, and its row m = 8a + 4h + b is
+// element 16h + 4a + b, so that a lane ends with 16 consecutive elements.
+
+typedef float float16v __attribute__((ext_vector_type(16)));
+
+// 16-byte slot of 8 elements of a staged key, and of the keys (t, h) of element
+// d of staged values; the low bits are exchanged so that the lanes that read
+// together meet different banks.
+template <int D>
+__device__ __forceinline__ int k_slot(int key, int s) { return key * (D / 8) + (s ^ (key & 7)); }
+__device__ __forceinline__ int v_slot(int d, int t, int h) {
+  return (d >> 1) * 8 + (d & 1) * 4 + ((2 * t + h) ^ (((d >> 1) & 1) | ((d >> 3) & 2)));
+}
+
+template <int CODE, int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_kernel(KvAttend A) {
+  constexpr int NG = D == 256 ? 1 : 2;           // groups of 32 keys staged at a time
+  constexpr int KS = D / 16, NB = D / 32;        // steps of the K product, blocks of 32 elements
+  constexpr int UG = 2 * D, NU = NG * UG / kThreads;   // 16-byte units of a group (of K, of V) and of a thread
+  __shared__ uint4 lds_k[2][NG][32 * D / 8];
+  __shared__ uint4 lds_v[2][NG][D * 4];
+  const KvView& kv = A.kv;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), n = lane & 31, h = lane >> 5;
+  const KvTile tile = A.prompts[blockIdx.x / kv.n_kv];
+  const int head = blockIdx.x % kv.n_kv;
+  const KvSeq sq = A.seqs[tile.s];
+  const int G = kv.n_heads / kv.n_kv, packed = sq.rows * G, r0 = tile.tile * kKvPromptRows;
+
+  // this lane's query row; rows past the last one repeat it and are not stored
+  const int r = r0 + wave * 32 + n, rr = min(r, packed - 1), t = rr / G;
+  const int pos = sq.start + t, lo = A.window ? max(0, pos - A.window + 1) : 0;
+  const int len = sq.start + sq.rows;
+  const int wg_first = sq.start + r0 / G, wg_last = sq.start + (min(r0 + kKvPromptRows, packed) - 1) / G;
+  const int w_first = uni(sq.start + min(r0 + wave * 32, packed - 1) / G);
+  const int w_last = uni(sq.start + min(r0 + wave * 32 + 31, packed - 1) / G);
+  const int w_lo = A.window ? max(0, w_first - A.window + 1) : 0, w_all = A.window ? max(0, w_last - A.window + 1) : 0;
+  half8 qf[KS];
+  {
+    const _Float16* q = (const _Float16*)A.q + (int64_t)(sq.row0 + t) * A.q_stride + (head * G + rr % G) * D;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) qf[k] = *(const half8*)(q + k * 16 + h * 8);
+  }
+  const int g_lo = (A.window ? max(0, wg_first - A.window + 1) : 0) / kKvGroup, g_hi = wg_last / kKvGroup + 1;
+  const int per = (g_hi - g_lo + tile.splits - 1) / tile.splits;
+  const int g_begin = uni(g_lo + tile.split * per), g_end = uni(min(g_hi, g_begin + per));
+  const int32_t* row = kv_row(kv, sq.seq, A.layer, head);
+  const int nb = kv.block / kKvGroup;
+
+  uint4 kc[NU], vc[NU];
+  float rk[NG], rv[NG], rk_next[NG], rv_next[NG];
+  // codes of groups g .. g + NG - 1 (those before g_end) and their ranges
+  auto load = [&](int g) {
+#pragma unroll
+    for (int x = 0; x < NG; ++x) {
+      const int gg = min(g + x, g_end - 1), b = gg / nb, sub = gg - b * nb;
+      const int32_t page = uni(row[b]);
+      const char* kb = kv.base + (int64_t)page * kv.page_bytes + (int64_t)sub * kKvGroup * D;
+      const char* vb = kb + (int64_t)kv.block * D;
+      rk_next[x] = kv.range[2 * (int64_t)page];
+      rv_next[x] = kv.range[2 * (int64_t)page + 1];
+      // unit u of the thread's NU belongs to group u * kThreads / UG
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const int at = u * kThreads + tid;
+        if (NG == 1 || (UG >= kThreads ? u * kThreads / UG == x : at / UG == x)) {
+          kc[u] = ld16(kb + (at % UG) * 16);
+          vc[u] = ld16(vb + (at % UG) * 16);
+        }
+      }
+    }
+  };
+  auto stage = [&](int buf, int g) {
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int at = u * kThreads + tid, x = at / UG, uu = at % UG;
+      const int key = uu / D * 16 + uu % 64 / 4, slot = uu % D / 64 * 8 + uu % 4 * 2;
+      lds_k[buf][x][k_slot<D>(key, slot)] = __builtin_bit_cast(uint4, Code<CODE>::halves(kc[u].x, kc[u].y));
+      lds_k[buf][x][k_slot<D>(key, slot + 1)] = __builtin_bit_cast(uint4, Code<CODE>::halves(kc[u].z, kc[u].w));
+      const int vg = uu % 64 / 16, d = uu / 64 * 32 + uu % 16 * 2;
+      uint4 c = vc[u];
+      // e4m3 bytes behind the sequence may be NaN, which a weight of zero keeps
+      if (CODE == SLORA_KV_FP8 && (g + x) * kKvGroup + kKvGroup > len) {
+        uint32_t keep[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((g + x) * kKvGroup + (j >> 2) * 16 + vg * 4 + (j & 3) < len) keep[j >> 2] |= 0xFFu << (8 * (j & 3));
+        c = make_uint4(c.x & keep[0], c.y & keep[1], c.z & keep[0], c.w & keep[1]);
+      }
+      const half8 even = Code<CODE>::halves(c.x, c.y), odd = Code<CODE>::halves(c.z, c.w);
+      // tokens 4 vg .. of either half of the group: keys (t, vg & 1), the lower or upper four of the slot
+      uint2* at_v = reinterpret_cast<uint2*>(lds_v[buf][x]);
+      const uint4 ev = __builtin_bit_cast(uint4, even), ov = __builtin_bit_cast(uint4, odd);
+      at_v[2 * v_slot(d, 0, vg & 1) + (vg >> 1)] = make_uint2(ev.x, ev.y);
+      at_v[2 * v_slot(d, 1, vg & 1) + (vg >> 1)] = make_uint2(ev.z, ev.w);
+      at_v[2 * v_slot(d + 1, 0, vg & 1) + (vg >> 1)] = make_uint2(ov.x, ov.y);
+      at_v[2 * v_slot(d + 1, 1, vg & 1) + (vg >> 1)] = make_uint2(ov.z, ov.w);
+    }
+#pragma unroll
+    for (int x = 0; x < NG; ++x) { rk[x] = rk_next[x]; rv[x] = rv_next[x]; }
+  };
+
+  float16v acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = float16v{};
+  float m = -FLT_MAX, l = 0.f, ref = 0.f;
+  const int vd = (n >> 2 & 1) * 16 + (n >> 3) * 4 + (n & 3);     // element of this lane's row of a block of V^T
+
+  if (g_begin < g_end) {
+    load(g_begin);
+    stage(0, g_begin);
+  }
+  lds_barrier();
+  int buf = 0;
+  for (int gb = g_begin; gb < g_end; gb += NG) {
+    const bool more = gb + NG < g_end;
+    if (more) load(gb + NG);
+#pragma unroll
+    for (int x = 0; x < NG; ++x) {
+      const int key0 = (gb + x) * kKvGroup;
+      if (gb + x >= g_end || key0 > w_last || key0 + kKvGroup <= w_lo) continue;
+      float16v s = {};
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            __builtin_bit_cast(half8, lds_k[buf][x][k_slot<D>(n, 2 * k + h)]), qf[k], s, 0, 0, 0);
+      const float ck = rk[x] / Code<CODE>::kTop * A.scale_log2;
+      bool seen = true;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[j] *= ck;
+      if (key0 + kKvGroup - 1 > w_first || key0 < w_all) {
+        seen = false;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int key = key0 + (j >> 2) * 8 + h * 4 + (j & 3);
+          const bool in = key <= pos && key >= lo;
+          s[j] = in ? s[j] : -INFINITY;
+          seen |= in;
+        }
+      }
+      float top = s[0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
+      if (__any(top > m + kLazy)) {
+        const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32))), f = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[b] *= f;
+      }
+      float unit = 1.f;
+      if (rv[x] > 0.f) {
+        unit = rv[x] / ref;
+        if (!(unit > 0x1p-10f && unit < 0x1p6f)) {
+          const float f = ref / rv[x];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[b] *= f;
+          ref = rv[x];
+          unit = 1.f;
+        }
+      }
+      half8 p[2];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float e = __builtin_amdgcn_exp2f(s[j] - m);
+        l += e;
+        p[j >> 3][j & 7] = (_Float16)(e * unit);
+      }
+      if (rv[x] != rv[x] && seen) l = __uint_as_float(0x7FC00000u);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+          acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              __builtin_bit_cast(half8, lds_v[buf][x][v_slot(b * 32 + vd, tt, h)]), p[tt], acc[b], 0, 0, 0);
+    }
+    if (more) {
+      stage(buf ^ 1, gb + NG);
+      lds_barrier();
+    }
+    buf ^= 1;
+  }
+  l += __shfl_xor(l, 32);
+  if (tile.splits > 1) {
+    // one slot for each 16 rows, as the row tiles'
+    const int64_t at = tile.part + (wave * 2 + (n >> 4)) * tile.splits + tile.split;
+    float* part = A.part + (at * kv.n_kv + head) * kv_part_floats(D);
+    const float f = ref / Code<CODE>::kTop;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *(float4v*)(part + (n & 15) * D + b * 32 + h * 16 + c * 4) =
+            float4v{acc[b][4 * c] * f, acc[b][4 * c + 1] * f, acc[b][4 * c + 2] * f, acc[b][4 * c + 3] * f};
+    if (h == 0) {
+      part[kKvRows * D + 2 * (n & 15)] = m;
+      part[kKvRows * D + 2 * (n & 15) + 1] = l;
+    }
+  } else if (r < packed) {
+    _Float16* out = (_Float16*)A.out + (int64_t)(sq.row0 + t) * A.out_stride + (head * G + rr % G) * D;
+    const float f = ref / Code<CODE>::kTop / l;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        half8 y;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = (_Float16)(acc[b][8 * c + j] * f);
+        *(half8*)(out + b * 32 + h * 16 + c * 8) = y;
+      }
+  }
+}
+
 // Joins the splits of a row tile: one workgroup per tile and kv head.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
@@ -923,6 +1144,11 @@ template <typename T>
 static const void* rows_of(int code, int dim) {
   return code == SLORA_KV_INT8 ? rows_of<T, SLORA_KV_INT8>(dim) : rows_of<T, SLORA_KV_FP8>(dim);
 }
+template <int CODE>
+static const void* prompt_of(int dim) {
+  return dim == 64 ? (const void*)kv_attend_prompt_kernel<CODE, 64>
+         : dim == 128 ? (const void*)kv_attend_prompt_kernel<CODE, 128> : (const void*)kv_attend_prompt_kernel<CODE, 256>;
+}
 template <typename T>
 static const void* combine_of(int dim) {
   return dim == 64 ? (const void*)kv_combine_kernel<T, 64>
@@ -945,7 +1171,10 @@ hipError_t launch_kv_append(const KvAppend& A0, hipStream_t stream) {
 
 hipError_t launch_kv_attend(const KvAttend& A, hipStream_t stream) {
   const bool half = A.kv.dtype == SLORA_F16;
-  hipError_t e = run(half ? rows_of<_Float16>(A.kv.code, A.kv.dim) : rows_of<float>(A.kv.code, A.kv.dim),
+  hipError_t e = run(A.kv.code == SLORA_KV_INT8 ? prompt_of<SLORA_KV_INT8>(A.kv.dim) : prompt_of<SLORA_KV_FP8>(A.kv.dim),
+                     (int64_t)A.n_prompts * A.kv.n_kv, A, stream);
+  if (e != hipSuccess) return e;
+  e = run(half ? rows_of<_Float16>(A.kv.code, A.kv.dim) : rows_of<float>(A.kv.code, A.kv.dim),
                      (int64_t)A.n_tiles * A.kv.n_kv, A, stream);
   if (e != hipSuccess) return e;
   return run(half ? combine_of<_Float16>(A.kv.dim) : combine_of<float>(A.kv.dim), (int64_t)A.n_combine * A.kv.n_kv, A,

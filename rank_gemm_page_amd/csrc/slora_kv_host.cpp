@@ -107,7 +107,7 @@ struct slora_kv_step {
   std::vector<int32_t> ends;       // blocks of each sequence at the end of the step
   std::vector<KvBlock> blocks;
   std::vector<int32_t> row_pos;
-  std::vector<KvTile> tiles, combine;
+  std::vector<KvTile> prompts, tiles, combine;
   std::vector<KvPatch> patches;
   int32_t n_rows = 0, max_len = 0, n_small = 0;
   int64_t n_new_pages = 0, n_parts = 0;
@@ -115,7 +115,8 @@ struct slora_kv_step {
 
   // byte offsets in the device metadata (every record is 16 bytes or more)
   size_t blocks_off() const { return seqs.size() * sizeof(KvSeq); }
-  size_t tiles_off() const { return blocks_off() + blocks.size() * sizeof(KvBlock); }
+  size_t prompts_off() const { return blocks_off() + blocks.size() * sizeof(KvBlock); }
+  size_t tiles_off() const { return prompts_off() + prompts.size() * sizeof(KvTile); }
   size_t patches_off() const { return tiles_off() + (tiles.size() + combine.size()) * sizeof(KvTile); }
   size_t row_pos_off() const { return patches_off() + patches.size() * sizeof(KvPatch); }
   size_t bytes() const { return row_pos_off() + row_pos.size() * sizeof(int32_t); }
@@ -129,18 +130,57 @@ namespace {
 // second the chip is full several times over.
 constexpr int64_t kMinGroups = 8, kWantGroups = 2048;
 
-// Row tiles of 16 packed rows with their key splits, longest first.
+// Sequences with at least this many packed rows (query heads of a kv head times
+// rows) take the prompt tiles (fp16), whose keys are split only where a launch
+// has fewer tiles than the chip holds twice over: a workgroup takes at least
+// kPromptGroups groups.
+constexpr int64_t kPromptMin = 64, kPromptGroups = 16, kWantPrompts = 1024;
+
+// Tiles of 128 packed rows for long runs of rows (fp16), and row tiles of 16 for
+// the others, with their key splits, longest first.
 void build_tiles(slora_kv_step* st) {
   const slora_kv_desc& d = st->kv->d;
   const int32_t G = d.n_heads / d.n_kv_heads;
+  const bool half = st->kv->info.dtype == SLORA_F16;
+  auto prompt = [&](const KvSeq& s) { return half && (int64_t)s.rows * G >= kPromptMin; };
+  // key groups that the tile of packed rows [r0, r0 + n) sees, without a window
+  auto groups_of = [&](const KvSeq& s, int64_t r0, int64_t n) {
+    return (s.start + (std::min<int64_t>(r0 + n, (int64_t)s.rows * G) - 1) / G) / kKvGroup + 1;
+  };
   int64_t total = 0;
+  for (const KvSeq& s : st->seqs)
+    for (int64_t r0 = 0; prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvPromptRows) total += groups_of(s, r0, kKvPromptRows);
+  const int64_t most = std::max<int64_t>(kPromptGroups, (total * d.n_kv_heads + kWantPrompts - 1) / kWantPrompts);
+  for (size_t i = 0; i < st->seqs.size(); ++i) {
+    const KvSeq& s = st->seqs[i];
+    const int64_t packed = (int64_t)s.rows * G;
+    if (!prompt(s)) continue;
+    for (int64_t t = 0; t * kKvPromptRows < packed; ++t) {
+      const int64_t groups = groups_of(s, t * kKvPromptRows, kKvPromptRows);
+      const int32_t splits = (int32_t)std::max<int64_t>(1, (groups + most / 2) / most);
+      KvTile tile{(int32_t)i, (int32_t)t, 0, splits, (int32_t)st->n_parts, {(int32_t)((groups + splits - 1) / splits), 0, 0}};
+      for (int32_t k = 0; k < splits; ++k) {
+        tile.split = k;
+        st->prompts.push_back(tile);
+      }
+      if (splits == 1) continue;
+      for (int32_t sub = 0; sub < kKvPromptRows / kKvRows; ++sub)
+        if (t * kKvPromptRows + sub * kKvRows < packed)
+          st->combine.push_back({(int32_t)i, (int32_t)(t * (kKvPromptRows / kKvRows)) + sub, 0, splits,
+                                 (int32_t)st->n_parts + sub * splits, {0, 0, 0}});
+      st->n_parts += (int64_t)splits * (kKvPromptRows / kKvRows);
+    }
+  }
+  total = 0;
   for (const KvSeq& s : st->seqs) {
+    if (prompt(s)) continue;
     const int64_t tiles = ((int64_t)s.rows * G + kKvRows - 1) / kKvRows;
     total += tiles * ((s.start + s.rows + kKvGroup - 1) / kKvGroup);
   }
   const int64_t chunk = std::max<int64_t>(kMinGroups, (total * d.n_kv_heads + kWantGroups - 1) / kWantGroups);
   for (size_t i = 0; i < st->seqs.size(); ++i) {
     const KvSeq& s = st->seqs[i];
+    if (prompt(s)) continue;
     const int64_t packed = (int64_t)s.rows * G;
     for (int64_t t = 0; t * kKvRows < packed; ++t) {
       const int64_t last = (std::min<int64_t>((t + 1) * kKvRows, packed) - 1) / G;   // token of the tile's last row
@@ -158,7 +198,9 @@ void build_tiles(slora_kv_step* st) {
       }
     }
   }
-  std::stable_sort(st->tiles.begin(), st->tiles.end(), [](const KvTile& a, const KvTile& b) { return a.pad[0] > b.pad[0]; });
+  auto longer = [](const KvTile& a, const KvTile& b) { return a.pad[0] > b.pad[0]; };
+  std::stable_sort(st->prompts.begin(), st->prompts.end(), longer);
+  std::stable_sort(st->tiles.begin(), st->tiles.end(), longer);
 }
 
 slora_status check_launch(const std::string& f, const slora_kv* kv, const slora_kv_step* st, int32_t layer) {
@@ -369,6 +411,7 @@ slora_status slora_kv_step_get_info(const slora_kv_step* st, slora_kv_step_info*
   info->n_blocks = (int32_t)st->blocks.size();
   info->n_new_pages = (int32_t)st->n_new_pages;
   info->n_row_tiles = (int32_t)st->tiles.size();
+  info->n_prompt_tiles = (int32_t)st->prompts.size();
   info->meta_bytes = st->bytes();
   info->workspace_bytes = st->workspace();
   return SLORA_OK;
@@ -394,6 +437,7 @@ slora_status slora_kv_step_upload(slora_kv_step* st, void* dev_meta, size_t dev_
     };
     put(0, st->seqs.data(), st->seqs.size() * sizeof(KvSeq));
     put(st->blocks_off(), st->blocks.data(), st->blocks.size() * sizeof(KvBlock));
+    put(st->prompts_off(), st->prompts.data(), st->prompts.size() * sizeof(KvTile));
     put(st->tiles_off(), st->tiles.data(), st->tiles.size() * sizeof(KvTile));
     put(st->tiles_off() + st->tiles.size() * sizeof(KvTile), st->combine.data(), st->combine.size() * sizeof(KvTile));
     put(st->patches_off(), st->patches.data(), st->patches.size() * sizeof(KvPatch));
@@ -484,6 +528,8 @@ slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* st, int32_t laye
   A.kv = kv->view();
   A.seqs = reinterpret_cast<const KvSeq*>(st->dev);
   A.tiles = reinterpret_cast<const KvTile*>(st->dev + st->tiles_off());
+  A.prompts = reinterpret_cast<const KvTile*>(st->dev + st->prompts_off());
+  A.n_prompts = (int32_t)st->prompts.size();
   A.n_tiles = (int32_t)st->tiles.size();
   A.n_combine = (int32_t)st->combine.size();
   A.layer = layer;
