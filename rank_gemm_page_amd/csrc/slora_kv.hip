@@ -820,8 +820,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
   {
     const _Float16* q = (const _Float16*)A.q + (int64_t)(sq.row0 + t) * A.q_stride + (head * G + rr % G) * D;
 #pragma unroll
-    for (int k = 0; k < KS; ++k) qf[k] = *(const half8*)(q + k * 16 + h * 8);
+    for (int k = 0; k < KS; ++k) {
+      qf[k] = *(const half8*)(q + k * 16 + h * 8);
+      if (A.scale_log2 < 0.f) qf[k] = -qf[k];
+    }
   }
+  const float scale = fabsf(A.scale_log2) / Code<CODE>::kTop;
   const int g_lo = (A.window ? max(0, wg_first - A.window + 1) : 0) / kKvGroup, g_hi = wg_last / kKvGroup + 1;
   const int per = (g_hi - g_lo + tile.splits - 1) / tile.splits;
   const int g_begin = uni(g_lo + tile.split * per), g_end = uni(min(g_hi, g_begin + per));
@@ -905,10 +909,11 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
       for (int k = 0; k < KS; ++k)
         s = __builtin_amdgcn_mfma_f32_32x32x16_f16(
             __builtin_bit_cast(half8, lds_k[buf][x][k_slot<D>(n, 2 * k + h)]), qf[k], s, 0, 0, 0);
-      const float ck = rk[x] / Code<CODE>::kTop * A.scale_log2;
+      // scores are s * ck with ck > 0 (q carries the scale's sign; a factor of 0
+      // would turn hidden keys into NaN)
+      float ck = rk[x] * scale;
+      ck = ck == 0.f ? FLT_MIN : ck;
       bool seen = true;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[j] *= ck;
       if (key0 + kKvGroup - 1 > w_first || key0 < w_all) {
         seen = false;
 #pragma unroll
@@ -922,6 +927,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
       float top = s[0];
 #pragma unroll
       for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
+      top *= ck;
       if (__any(top > m + kLazy)) {
         const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32))), f = __builtin_amdgcn_exp2f(m - mn);
         m = mn;
@@ -929,9 +935,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[b] *= f;
       }
+      // values of a block count in units of its range: sums are kept in units of
+      // a reference range, replaced when a block's is far from it.  The weights
+      // carry the factor in their exponent, and their sum is freed of it.
       float unit = 1.f;
       if (rv[x] > 0.f) {
-        unit = rv[x] / ref;
+        unit = rv[x] * __builtin_amdgcn_rcpf(ref);
         if (!(unit > 0x1p-10f && unit < 0x1p6f)) {
           const float f = ref / rv[x];
 #pragma unroll
@@ -940,13 +949,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
           unit = 1.f;
         }
       }
+      const float shift = __builtin_amdgcn_logf(unit) - m;
+      float sum = 0.f;
       half8 p[2];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float e = __builtin_amdgcn_exp2f(s[j] - m);
-        l += e;
-        p[j >> 3][j & 7] = (_Float16)(e * unit);
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], ck, shift));
+        sum += e;
+        p[j >> 3][j & 7] = (_Float16)e;
       }
+      l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(unit), l);
       if (rv[x] != rv[x] && seen) l = __uint_as_float(0x7FC00000u);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
