@@ -786,12 +786,12 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
 typedef float float16v __attribute__((ext_vector_type(16)));
 
 // 16-byte slot of 8 elements of a staged key, and of the keys (t, h) of element
-// d of staged values; the low bits are exchanged so that the lanes that read
-// together meet different banks.
+// d of staged values; the low bits are exchanged so that the lanes that read or
+// write together meet different banks.
 template <int D>
 __device__ __forceinline__ int k_slot(int key, int s) { return key * (D / 8) + (s ^ (key & 7)); }
 __device__ __forceinline__ int v_slot(int d, int t, int h) {
-  return (d >> 1) * 8 + (d & 1) * 4 + ((2 * t + h) ^ (((d >> 1) & 1) | ((d >> 3) & 2)));
+  return (d >> 1) * 8 + (((d & 1) * 4 + 2 * t + h) ^ (((d >> 1) & 5) | (((d >> 1) ^ (d >> 3)) & 2)));
 }
 
 template <int CODE, int D>
@@ -872,14 +872,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
           if ((g + x) * kKvGroup + (j >> 2) * 16 + vg * 4 + (j & 3) < len) keep[j >> 2] |= 0xFFu << (8 * (j & 3));
         c = make_uint4(c.x & keep[0], c.y & keep[1], c.z & keep[0], c.w & keep[1]);
       }
-      const half8 even = Code<CODE>::halves(c.x, c.y), odd = Code<CODE>::halves(c.z, c.w);
-      // tokens 4 vg .. of either half of the group: keys (t, vg & 1), the lower or upper four of the slot
-      uint2* at_v = reinterpret_cast<uint2*>(lds_v[buf][x]);
-      const uint4 ev = __builtin_bit_cast(uint4, even), ov = __builtin_bit_cast(uint4, odd);
-      at_v[2 * v_slot(d, 0, vg & 1) + (vg >> 1)] = make_uint2(ev.x, ev.y);
-      at_v[2 * v_slot(d, 1, vg & 1) + (vg >> 1)] = make_uint2(ev.z, ev.w);
-      at_v[2 * v_slot(d + 1, 0, vg & 1) + (vg >> 1)] = make_uint2(ov.x, ov.y);
-      at_v[2 * v_slot(d + 1, 1, vg & 1) + (vg >> 1)] = make_uint2(ov.z, ov.w);
+      // lanes vg and vg + 2 (32 apart) hold the two quads of tokens of a slot: the
+      // lower lane takes those of the group's first half, the upper the second's
+      const auto even = __builtin_amdgcn_permlane32_swap(c.x, c.y, false, false);
+      const auto odd = __builtin_amdgcn_permlane32_swap(c.z, c.w, false, false);
+      lds_v[buf][x][v_slot(d, vg >> 1, vg & 1)] = __builtin_bit_cast(uint4, Code<CODE>::halves(even[0], even[1]));
+      lds_v[buf][x][v_slot(d + 1, vg >> 1, vg & 1)] = __builtin_bit_cast(uint4, Code<CODE>::halves(odd[0], odd[1]));
     }
 #pragma unroll
     for (int x = 0; x < NG; ++x) { rk[x] = rk_next[x]; rv[x] = rv_next[x]; }
