@@ -786,12 +786,15 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
 typedef float float16v __attribute__((ext_vector_type(16)));
 
 // 16-byte slot of 8 elements of a staged key, and of the keys (t, h) of element
-// d of staged values; the low bits are exchanged so that the lanes that read or
-// write together meet different banks.
+// d of staged values; the low bits are exchanged so that the 16 lanes that read
+// or write together meet all 64 banks.
 template <int D>
-__device__ __forceinline__ int k_slot(int key, int s) { return key * (D / 8) + (s ^ (key & 7)); }
+__device__ __forceinline__ int k_slot(int key, int s) {
+  return key * (D / 8) + (s ^ (D == 64 ? key >> 1 & 7 : key & 15));
+}
 __device__ __forceinline__ int v_slot(int d, int t, int h) {
-  return (d >> 1) * 8 + (((d & 1) * 4 + 2 * t + h) ^ (((d >> 1) & 5) | (((d >> 1) ^ (d >> 3)) & 2)));
+  const int p = d >> 1;
+  return p * 8 + (((d & 1) * 4 + 2 * t + h) ^ ((p >> 1 & 1) | (p >> 2 & 2) | (p & 4)));
 }
 
 template <int CODE, int D>
