@@ -910,10 +910,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
       for (int k = 0; k < KS; ++k)
         s = __builtin_amdgcn_mfma_f32_32x32x16_f16(
             __builtin_bit_cast(half8, lds_k[buf][x][k_slot<D>(n, 2 * k + h)]), qf[k], s, 0, 0, 0);
-      // scores are s * ck with ck > 0 (q carries the scale's sign; a factor of 0
-      // would turn hidden keys into NaN)
+      // scores are s * ck with ck > 0: q carries the scale's sign, and a factor
+      // of 0 or NaN would give hidden keys a weight
       float ck = rk[x] * scale;
-      ck = ck == 0.f ? FLT_MIN : ck;
+      ck = ck > 0.f ? ck : FLT_MIN;
       bool seen = true;
       if (key0 + kKvGroup - 1 > w_first || key0 < w_all) {
         seen = false;
@@ -960,7 +960,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
         p[j >> 3][j & 7] = (_Float16)e;
       }
       l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(unit), l);
-      if (rv[x] != rv[x] && seen) l = __uint_as_float(0x7FC00000u);
+      // a block whose range is NaN holds zero codes; the rows that see it are NaN
+      if ((rk[x] != rk[x] || rv[x] != rv[x]) && seen) l = __uint_as_float(0x7FC00000u);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll

@@ -124,6 +124,24 @@ def test_values_that_are_not_finite_mark_their_block_and_head(dtype, code, what)
         c.check_read([0])
 
 
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("window", [0, 9])
+def test_rows_beside_a_marked_block(code, what, window):
+    """Rows of one tile on both sides of a block that reads as NaN: those that do not see it are numbers."""
+    with KvCase(torch, "f16", code, 8, 2, 64, 32) as c:
+        c.append([0], [25])
+        k, v = c.draw(60, 2), c.draw(60, 2)
+        (k if what == "k" else v)[40 - 25, :, 3] = np.inf              # in block 1: positions 32 .. 63
+        st, info, ws, q, starts = c.append([0], [60], k=k, v=v)
+        got = c.attend(st, q, ws, 0.125, window).cpu().numpy()
+        pos = 25 + np.arange(60)
+        sees = (pos >= 32) & ((pos - window + 1 <= 63) if window else True)
+        assert np.isnan(got[sees]).all() and np.isfinite(got[~sees]).all()
+        want, *_ = c.model.attend(0, 0, q.cpu().numpy(), 25, 0.125, window)
+        assert np.abs(got[~sees] - want[~sees]).max() < 2e-2
+
+
 def test_rows_behind_the_last_sequence_stay_as_they_were():
     with KvCase(torch, "f16", 0, 4, 2, 64, 32) as c:
         st, info, ws, q, starts = c.append([0, 2], [5, 40])
