@@ -1006,39 +1006,53 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
   }
 }
 
-// Joins the splits of a row tile: one workgroup per tile and kv head.
+// Joins the splits of a row tile: one workgroup per row.  D / 4 threads read a
+// split's row, so 1024 / D splits are read side by side and then joined in LDS.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
-  constexpr int PER = D / 16;
+  constexpr int TR = D / 4, NS = kThreads / TR;
+  __shared__ float lds_o[NS][D];
+  __shared__ float lds_m[NS], lds_l[NS];
   const KvView& kv = A.kv;
-  const KvTile tile = A.tiles[A.n_tiles + blockIdx.x / kv.n_kv];
-  const int head = blockIdx.x % kv.n_kv;
+  const int tid = threadIdx.x, orow = blockIdx.x % kKvRows, at = blockIdx.x / kKvRows;
+  const KvTile tile = A.tiles[A.n_tiles + at / kv.n_kv];
+  const int head = at % kv.n_kv;
   const KvSeq sq = A.seqs[tile.s];
-  const int G = kv.n_heads / kv.n_kv, tid = threadIdx.x, orow = tid >> 4, od = (tid & 15) * PER;
-  const int gr = tile.tile * kKvRows + orow;
+  const int G = kv.n_heads / kv.n_kv, gr = tile.tile * kKvRows + orow, side = tid / TR, d = tid % TR * 4;
   if (gr >= sq.rows * G) return;
   const int64_t step = kv.n_kv * kv_part_floats(D);
   const float* part = A.part + ((int64_t)tile.part * kv.n_kv + head) * kv_part_floats(D);
-  float mm = -FLT_MAX;
-  for (int s = 0; s < tile.splits; ++s) mm = fmaxf(mm, part[s * step + kKvRows * D + 2 * orow]);
-  float ll = 0.f, o[PER];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) o[j] = 0.f;
-  for (int s = 0; s < tile.splits; ++s) {
+  float m = -FLT_MAX, l = 0.f;
+  float4v o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = side; s < tile.splits; s += NS) {
     const float* ps = part + s * step;
-    const float f = __builtin_amdgcn_exp2f(ps[kKvRows * D + 2 * orow] - mm);
-    ll += f * ps[kKvRows * D + 2 * orow + 1];
-#pragma unroll
-    for (int j = 0; j < PER; j += 4) {
-      const float4v x = *(const float4v*)(ps + orow * D + od + j);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) o[j + c] += f * x[c];
-    }
+    const float ms = ps[kKvRows * D + 2 * orow], ls = ps[kKvRows * D + 2 * orow + 1];
+    const float4v x = *(const float4v*)(ps + orow * D + d);
+    const float mn = fmaxf(m, ms), f = __builtin_amdgcn_exp2f(m - mn), fs = __builtin_amdgcn_exp2f(ms - mn);
+    m = mn;
+    l = l * f + ls * fs;
+    o = o * f + x * fs;
   }
-  T* out = (T*)A.out + (int64_t)(sq.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + od;
+  *(float4v*)&lds_o[side][d] = o;
+  if (d == 0) { lds_m[side] = m; lds_l[side] = l; }
+  __syncthreads();
+  if (side) return;
+  float mm = lds_m[0];
+#pragma unroll
+  for (int s = 1; s < NS; ++s) mm = fmaxf(mm, lds_m[s]);
+  float ll = 0.f;
+  o = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const float f = __builtin_amdgcn_exp2f(lds_m[s] - mm);
+    ll += f * lds_l[s];
+    o += f * *(const float4v*)&lds_o[s][d];
+  }
+  T* out = (T*)A.out + (int64_t)(sq.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + d;
   const float inv = 1.f / ll;
 #pragma unroll
-  for (int j = 0; j < PER; ++j) out[j] = (T)(o[j] * inv);
+  for (int j = 0; j < 4; ++j) out[j] = (T)(o[j] * inv);
 }
 
 // ---------------------------------------------------------------------------
@@ -1191,8 +1205,8 @@ hipError_t launch_kv_attend(const KvAttend& A, hipStream_t stream) {
   e = run(half ? rows_of<_Float16>(A.kv.code, A.kv.dim) : rows_of<float>(A.kv.code, A.kv.dim),
                      (int64_t)A.n_tiles * A.kv.n_kv, A, stream);
   if (e != hipSuccess) return e;
-  return run(half ? combine_of<_Float16>(A.kv.dim) : combine_of<float>(A.kv.dim), (int64_t)A.n_combine * A.kv.n_kv, A,
-             stream);
+  return run(half ? combine_of<_Float16>(A.kv.dim) : combine_of<float>(A.kv.dim), (int64_t)A.n_combine * A.kv.n_kv * kKvRows,
+             A, stream);
 }
 
 hipError_t launch_kv_read(const KvRead& R, hipStream_t stream) {

@@ -171,13 +171,21 @@ void build_tiles(slora_kv_step* st) {
       st->n_parts += (int64_t)splits * (kKvPromptRows / kKvRows);
     }
   }
-  total = 0;
-  for (const KvSeq& s : st->seqs) {
-    if (prompt(s)) continue;
-    const int64_t tiles = ((int64_t)s.rows * G + kKvRows - 1) / kKvRows;
-    total += tiles * ((s.start + s.rows + kKvGroup - 1) / kKvGroup);
+  // groups of a workgroup: the fewest for which all row tiles' workgroups are at most kWantGroups
+  std::vector<int64_t> lens;
+  for (const KvSeq& s : st->seqs)
+    for (int64_t r0 = 0; !prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvRows) lens.push_back(groups_of(s, r0, kKvRows));
+  int64_t chunk = kMinGroups;
+  if (!lens.empty()) {
+    int64_t high = std::max(chunk, *std::max_element(lens.begin(), lens.end()));
+    while (chunk < high) {
+      const int64_t mid = (chunk + high) / 2;
+      int64_t wgs = 0;
+      for (int64_t n : lens) wgs += (n + mid - 1) / mid;
+      if (wgs * d.n_kv_heads <= kWantGroups) high = mid;
+      else chunk = mid + 1;
+    }
   }
-  const int64_t chunk = std::max<int64_t>(kMinGroups, (total * d.n_kv_heads + kWantGroups - 1) / kWantGroups);
   for (size_t i = 0; i < st->seqs.size(); ++i) {
     const KvSeq& s = st->seqs[i];
     if (prompt(s)) continue;
@@ -358,7 +366,8 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
                             }) - st->blocks.begin());
     build_tiles(st);
     // every workgroup index of a launch is 31 bits
-    const int64_t most = std::max({2 * (int64_t)st->blocks.size(), (int64_t)st->tiles.size(), st->n_parts}) * kv->d.n_kv_heads +
+    const int64_t most = std::max({2 * (int64_t)st->blocks.size(), (int64_t)st->tiles.size(), (int64_t)st->combine.size() * kKvRows, st->n_parts}) *
+                             kv->d.n_kv_heads +
                          rows * kv->d.n_heads * kv->d.head_dim / 16 / kThreads;
     if (most > INT32_MAX / 2 || rows * kv->d.n_heads > INT32_MAX / 2 || patches > INT32_MAX / 2) {
       delete st;
