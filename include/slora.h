@@ -622,8 +622,10 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* step, int32_t la
  * is held in fp32, and out is rounded once to the pool dtype.  q is [n_rows]
  * rotated rows (slora_kv_append's q_out), q and out laid out as for
  * slora_kv_append.  workspace is device memory of at least workspace_bytes,
- * 16-byte aligned (may be NULL when that is 0); launches that may run at the
- * same time need workspaces of their own.  Launches on `stream` and returns without waiting. */
+ * 16-byte aligned (may be NULL when that is 0), and needs no clearing.
+ * Launches on `stream` and returns without waiting.  Where a sequence's keys are split over
+ * workgroups they count themselves in the step's metadata: attention launches
+ * of one step, captured ones included, run one after another. */
 slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* step, int32_t layer, const void* q,
                              int64_t q_stride, void* out, int64_t out_stride, float scale, int32_t window,
                              void* workspace, size_t workspace_bytes, void* stream);

@@ -45,8 +45,10 @@ struct KvTile { int32_t s, tile, split, splits, part, pad[3]; };   // rows tile*
 struct KvPatch { uint32_t lo, hi; int32_t page, pad; };      // page table entry (hi:lo) = page
 
 // A tile whose keys are split writes, per kv head, kKvRows x dim fp32 sums and
-// kKvRows (maximum, sum) pairs to slot (part + split) * n_kv + head; a combine
-// entry (the tile's record with split 0) joins the slots.
+// kKvRows (maximum, sum) pairs to slot (part + split) * n_kv + head.  The last
+// workgroup of a row tile joins its slots, by the counter at part * n_kv + head;
+// a prompt tile has the slots of its eight runs of 16 rows one after another,
+// and a combine entry (split 0) for each.
 constexpr int64_t kv_part_floats(int dim) { return (int64_t)kKvRows * (dim + 2); }
 
 struct KvAppend {
@@ -65,7 +67,9 @@ struct KvAttend {
   KvView kv;
   const KvSeq* seqs;
   const KvTile* prompts;      // tiles of a long run of rows (fp16)
-  const KvTile* tiles;        // row tiles, then (from n_tiles on) the combine entries
+  const KvTile* tiles;        // row tiles
+  const KvTile* combine;      // of split prompt tiles
+  uint32_t* counters;         // of split row tiles: zero before and after every launch
   int32_t n_prompts, n_tiles, n_combine, layer, window;
   const void* q; void* out;
   int64_t q_stride, out_stride;

@@ -562,6 +562,36 @@ __device__ __forceinline__ float8v frag8(const float* p, float8v*) {
 // reduction across lanes and no rescaling of the sums.
 constexpr float kLazy = 8.f;
 
+// Joining the key splits of a row tile in the same launch: every split's
+// workgroup writes its sums where all of them can see them (agent-scope atomic
+// stores, which are done at the level that the XCDs share), waits until they are
+// there, and counts itself; the one that finds the others counted joins all
+// sums, read at that level too, in the order of the splits, and sets the counter
+// back for the next launch.  No cache has to be written back or dropped for
+// this: with an acquire-release counter, which does both, 12 long conversations
+// took 196 us instead of 120.  One launch instead of two: 7.5 us instead of 8.4
+// for a single token.
+typedef unsigned long long u64;
+__device__ __forceinline__ void put_shared(float* p, float a, float b) {
+  const u64 w = (u64)__float_as_uint(b) << 32 | __float_as_uint(a);
+  __hip_atomic_store(reinterpret_cast<u64*>(p), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2v get_shared(const float* p) {
+  const u64 w = __hip_atomic_load(reinterpret_cast<const u64*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return float2v{__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
+}
+__device__ __forceinline__ bool last_of(uint32_t* counter, int splits, uint32_t* lds) {
+  __builtin_amdgcn_s_waitcnt(0);                 // this wave's sums are where the others see them
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint32_t before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (before == (uint32_t)splits - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *lds = before;
+  }
+  __syncthreads();
+  return *lds == (uint32_t)splits - 1;
+}
+
 template <typename T, int CODE, int D>
 __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
   using F = typename Frag<T>::type;
@@ -570,6 +600,7 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
   __shared__ float lds_o[4][kKvRows][DC + 4];
   __shared__ float lds_ml[4][kKvRows][2];
   __shared__ float lds_ref[4];
+  __shared__ uint32_t lds_last;
   const KvView& kv = A.kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), i = lane & 15, g = lane >> 4;
   const KvTile tile = A.tiles[blockIdx.x / kv.n_kv];
@@ -756,11 +787,10 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
       for (int j = 0; j < PER; ++j) o[j] += fo * lds_o[w][orow][od + j];
     }
     if (part) {
+      if (gr < packed) {
 #pragma unroll
-      for (int j = 0; j < PER; j += 4) *(float4v*)(part + orow * D + c0 + od + j) = float4v{o[j], o[j + 1], o[j + 2], o[j + 3]};
-      if (c0 == 0 && (tid & 15) == 0) {
-        part[kKvRows * D + 2 * orow] = mm;
-        part[kKvRows * D + 2 * orow + 1] = ll;
+        for (int j = 0; j < PER; j += 2) put_shared(part + orow * D + c0 + od + j, o[j], o[j + 1]);
+        if (c0 == 0 && (tid & 15) == 0) put_shared(part + kKvRows * D + 2 * orow, mm, ll);
       }
     } else if (gr < packed) {
       T* out = (T*)A.out + (int64_t)(sq.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + c0 + od;
@@ -768,6 +798,33 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) out[j] = (T)(o[j] * inv);
     }
+  }
+  if (!part || !last_of(A.counters + (int64_t)tile.part * kv.n_kv + head, tile.splits, &lds_last)) return;
+  if (gr >= packed) return;
+  const int64_t step = kv.n_kv * kv_part_floats(D);
+  part = A.part + ((int64_t)tile.part * kv.n_kv + head) * kv_part_floats(D);
+#pragma unroll
+  for (int c0 = 0; c0 < D; c0 += DC) {
+    float mm = -FLT_MAX, ll = 0.f, o[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) o[j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < tile.splits; ++k) {
+      const float* ps = part + k * step;
+      const float2v ml = get_shared(ps + kKvRows * D + 2 * orow);
+      float2v x[PER / 2];
+#pragma unroll
+      for (int j = 0; j < PER / 2; ++j) x[j] = get_shared(ps + orow * D + c0 + od + 2 * j);
+      const float mn = fmaxf(mm, ml[0]), f = __builtin_amdgcn_exp2f(mm - mn), fs = __builtin_amdgcn_exp2f(ml[0] - mn);
+      mm = mn;
+      ll = ll * f + ml[1] * fs;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) o[j] = o[j] * f + x[j / 2][j & 1] * fs;
+    }
+    T* out = (T*)A.out + (int64_t)(sq.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + c0 + od;
+    const float inv = 1.f / ll;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) out[j] = (T)(o[j] * inv);
   }
 }
 
@@ -1006,7 +1063,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
   }
 }
 
-// Joins the splits of a row tile: one workgroup per row.  D / 4 threads read a
+// Joins the splits of a prompt tile, 16 rows of it at a time: one workgroup per row.  D / 4 threads read a
 // split's row, so 1024 / D splits are read side by side and then joined in LDS.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
@@ -1015,7 +1072,7 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
   __shared__ float lds_m[NS], lds_l[NS];
   const KvView& kv = A.kv;
   const int tid = threadIdx.x, orow = blockIdx.x % kKvRows, at = blockIdx.x / kKvRows;
-  const KvTile tile = A.tiles[A.n_tiles + at / kv.n_kv];
+  const KvTile tile = A.combine[at / kv.n_kv];
   const int head = at % kv.n_kv;
   const KvSeq sq = A.seqs[tile.s];
   const int G = kv.n_heads / kv.n_kv, gr = tile.tile * kKvRows + orow, side = tid / TR, d = tid % TR * 4;

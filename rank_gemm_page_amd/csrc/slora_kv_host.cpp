@@ -110,7 +110,8 @@ struct slora_kv_step {
   std::vector<KvTile> prompts, tiles, combine;
   std::vector<KvPatch> patches;
   int32_t n_rows = 0, max_len = 0, n_small = 0;
-  int64_t n_new_pages = 0, n_parts = 0;
+  int64_t n_new_pages = 0;
+  int64_t n_parts = 0, n_row_parts = 0;   // slots of split tiles, those of row tiles first
   const char* dev = nullptr;
 
   // byte offsets in the device metadata (every record is 16 bytes or more)
@@ -119,7 +120,8 @@ struct slora_kv_step {
   size_t tiles_off() const { return prompts_off() + prompts.size() * sizeof(KvTile); }
   size_t patches_off() const { return tiles_off() + (tiles.size() + combine.size()) * sizeof(KvTile); }
   size_t row_pos_off() const { return patches_off() + patches.size() * sizeof(KvPatch); }
-  size_t bytes() const { return row_pos_off() + row_pos.size() * sizeof(int32_t); }
+  size_t counters_off() const { return row_pos_off() + row_pos.size() * sizeof(int32_t); }
+  size_t bytes() const { return counters_off() + (size_t)n_row_parts * kv->d.n_kv_heads * sizeof(uint32_t); }
   size_t workspace() const { return (size_t)n_parts * kv->d.n_kv_heads * kv_part_floats(kv->d.head_dim) * sizeof(float); }
 };
 
@@ -147,30 +149,6 @@ void build_tiles(slora_kv_step* st) {
   auto groups_of = [&](const KvSeq& s, int64_t r0, int64_t n) {
     return (s.start + (std::min<int64_t>(r0 + n, (int64_t)s.rows * G) - 1) / G) / kKvGroup + 1;
   };
-  int64_t total = 0;
-  for (const KvSeq& s : st->seqs)
-    for (int64_t r0 = 0; prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvPromptRows) total += groups_of(s, r0, kKvPromptRows);
-  const int64_t most = std::max<int64_t>(kPromptGroups, (total * d.n_kv_heads + kWantPrompts - 1) / kWantPrompts);
-  for (size_t i = 0; i < st->seqs.size(); ++i) {
-    const KvSeq& s = st->seqs[i];
-    const int64_t packed = (int64_t)s.rows * G;
-    if (!prompt(s)) continue;
-    for (int64_t t = 0; t * kKvPromptRows < packed; ++t) {
-      const int64_t groups = groups_of(s, t * kKvPromptRows, kKvPromptRows);
-      const int32_t splits = (int32_t)std::max<int64_t>(1, (groups + most / 2) / most);
-      KvTile tile{(int32_t)i, (int32_t)t, 0, splits, (int32_t)st->n_parts, {(int32_t)((groups + splits - 1) / splits), 0, 0}};
-      for (int32_t k = 0; k < splits; ++k) {
-        tile.split = k;
-        st->prompts.push_back(tile);
-      }
-      if (splits == 1) continue;
-      for (int32_t sub = 0; sub < kKvPromptRows / kKvRows; ++sub)
-        if (t * kKvPromptRows + sub * kKvRows < packed)
-          st->combine.push_back({(int32_t)i, (int32_t)(t * (kKvPromptRows / kKvRows)) + sub, 0, splits,
-                                 (int32_t)st->n_parts + sub * splits, {0, 0, 0}});
-      st->n_parts += (int64_t)splits * (kKvPromptRows / kKvRows);
-    }
-  }
   // groups of a workgroup: the fewest for which all row tiles' workgroups are at most kWantGroups
   std::vector<int64_t> lens;
   for (const KvSeq& s : st->seqs)
@@ -199,11 +177,32 @@ void build_tiles(slora_kv_step* st) {
         tile.split = k;
         st->tiles.push_back(tile);
       }
-      if (splits > 1) {
-        tile.split = 0;
-        st->combine.push_back(tile);
-        st->n_parts += splits;
+      if (splits > 1) st->n_parts += splits;
+    }
+  }
+  st->n_row_parts = st->n_parts;
+  int64_t total = 0;
+  for (const KvSeq& s : st->seqs)
+    for (int64_t r0 = 0; prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvPromptRows) total += groups_of(s, r0, kKvPromptRows);
+  const int64_t most = std::max<int64_t>(kPromptGroups, (total * d.n_kv_heads + kWantPrompts - 1) / kWantPrompts);
+  for (size_t i = 0; i < st->seqs.size(); ++i) {
+    const KvSeq& s = st->seqs[i];
+    const int64_t packed = (int64_t)s.rows * G;
+    if (!prompt(s)) continue;
+    for (int64_t t = 0; t * kKvPromptRows < packed; ++t) {
+      const int64_t groups = groups_of(s, t * kKvPromptRows, kKvPromptRows);
+      const int32_t splits = (int32_t)std::max<int64_t>(1, (groups + most / 2) / most);
+      KvTile tile{(int32_t)i, (int32_t)t, 0, splits, (int32_t)st->n_parts, {(int32_t)((groups + splits - 1) / splits), 0, 0}};
+      for (int32_t k = 0; k < splits; ++k) {
+        tile.split = k;
+        st->prompts.push_back(tile);
       }
+      if (splits == 1) continue;
+      for (int32_t sub = 0; sub < kKvPromptRows / kKvRows; ++sub)
+        if (t * kKvPromptRows + sub * kKvRows < packed)
+          st->combine.push_back({(int32_t)i, (int32_t)(t * (kKvPromptRows / kKvRows)) + sub, 0, splits,
+                                 (int32_t)st->n_parts + sub * splits, {0, 0, 0}});
+      st->n_parts += (int64_t)splits * (kKvPromptRows / kKvRows);
     }
   }
   auto longer = [](const KvTile& a, const KvTile& b) { return a.pad[0] > b.pad[0]; };
@@ -540,6 +539,8 @@ slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* st, int32_t laye
   A.prompts = reinterpret_cast<const KvTile*>(st->dev + st->prompts_off());
   A.n_prompts = (int32_t)st->prompts.size();
   A.n_tiles = (int32_t)st->tiles.size();
+  A.combine = A.tiles + A.n_tiles;
+  A.counters = reinterpret_cast<uint32_t*>(const_cast<char*>(st->dev + st->counters_off()));
   A.n_combine = (int32_t)st->combine.size();
   A.layer = layer;
   A.window = window;
