@@ -39,9 +39,10 @@ struct KvView {
 };
 
 // Records of a step (device metadata, int32 words).
-struct KvSeq { int32_t seq, start, rows, row0; };            // sequence id, first position, rows, first batch row
 struct KvBlock { int32_t seq, block, slot0, slot1, row, pad[3]; };   // sequence id, block, its slots [slot0, slot1) among the rows, batch row of slot0
-struct KvTile { int32_t s, tile, split, splits, part, pad[3]; };   // rows tile*16.. of the sequence's packed rows; part: see below
+// A tile of a sequence's packed rows: number, key split of how many, slots (see below); and the sequence: its first
+// row's position, its rows, the batch row of the first.
+struct KvTile { int32_t seq, tile, split, splits, part, start, rows, row0; };
 struct KvPatch { uint32_t lo, hi; int32_t page, pad; };      // page table entry (hi:lo) = page
 
 // A tile whose keys are split writes, per kv head, kKvRows x dim fp32 sums and
@@ -65,7 +66,6 @@ struct KvAppend {
 
 struct KvAttend {
   KvView kv;
-  const KvSeq* seqs;
   const KvTile* prompts;      // tiles of a long run of rows (fp16)
   const KvTile* tiles;        // row tiles
   const KvTile* combine;      // of split prompt tiles

@@ -605,21 +605,20 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), i = lane & 15, g = lane >> 4;
   const KvTile tile = A.tiles[blockIdx.x / kv.n_kv];
   const int head = blockIdx.x % kv.n_kv;
-  const KvSeq sq = A.seqs[tile.s];
-  const int G = kv.n_heads / kv.n_kv, packed = sq.rows * G;
+  const int G = kv.n_heads / kv.n_kv, packed = tile.rows * G;
 
   // this lane's query row (rows past the last one repeat it and are not stored)
   const int r = min(tile.tile * kKvRows + i, packed - 1);
-  const int t = r / G, pos = sq.start + t;
+  const int t = r / G, pos = tile.start + t;
   const int lo = A.window ? max(0, pos - A.window + 1) : 0;
   const int t_first = tile.tile * kKvRows / G, t_last = (min(tile.tile * kKvRows + kKvRows, packed) - 1) / G;
-  const int pos_first = sq.start + t_first, pos_last = sq.start + t_last, len = sq.start + sq.rows;
+  const int pos_first = tile.start + t_first, pos_last = tile.start + t_last, len = tile.start + tile.rows;
   const int tile_lo = A.window ? max(0, pos_first - A.window + 1) : 0;
   const int all_lo = A.window ? max(0, pos_last - A.window + 1) : 0;
 
   F qf[2 * NC];
   {
-    const T* q = (const T*)A.q + (int64_t)(sq.row0 + t) * A.q_stride + (head * G + r % G) * D;
+    const T* q = (const T*)A.q + (int64_t)(tile.row0 + t) * A.q_stride + (head * G + r % G) * D;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -634,7 +633,7 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
   int gi = uni(s_lo + wave * per_wave);
   const int ge = uni(min(s_hi, gi + per_wave));
 
-  const int32_t* row = kv_row(kv, sq.seq, A.layer, head);
+  const int32_t* row = kv_row(kv, tile.seq, A.layer, head);
   const int nb = kv.block / kKvGroup;
   float4v acc[NT];
 #pragma unroll
@@ -793,7 +792,7 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
         if (c0 == 0 && (tid & 15) == 0) put_shared(part + kKvRows * D + 2 * orow, mm, ll);
       }
     } else if (gr < packed) {
-      T* out = (T*)A.out + (int64_t)(sq.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + c0 + od;
+      T* out = (T*)A.out + (int64_t)(tile.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + c0 + od;
       const float inv = 1.f / ll;
 #pragma unroll
       for (int j = 0; j < PER; ++j) out[j] = (T)(o[j] * inv);
@@ -821,7 +820,7 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) o[j] = o[j] * f + x[j / 2][j & 1] * fs;
     }
-    T* out = (T*)A.out + (int64_t)(sq.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + c0 + od;
+    T* out = (T*)A.out + (int64_t)(tile.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + c0 + od;
     const float inv = 1.f / ll;
 #pragma unroll
     for (int j = 0; j < PER; ++j) out[j] = (T)(o[j] * inv);
@@ -865,20 +864,19 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), n = lane & 31, h = lane >> 5;
   const KvTile tile = A.prompts[blockIdx.x / kv.n_kv];
   const int head = blockIdx.x % kv.n_kv;
-  const KvSeq sq = A.seqs[tile.s];
-  const int G = kv.n_heads / kv.n_kv, packed = sq.rows * G, r0 = tile.tile * kKvPromptRows;
+  const int G = kv.n_heads / kv.n_kv, packed = tile.rows * G, r0 = tile.tile * kKvPromptRows;
 
   // this lane's query row; rows past the last one repeat it and are not stored
   const int r = r0 + wave * 32 + n, rr = min(r, packed - 1), t = rr / G;
-  const int pos = sq.start + t, lo = A.window ? max(0, pos - A.window + 1) : 0;
-  const int len = sq.start + sq.rows;
-  const int wg_first = sq.start + r0 / G, wg_last = sq.start + (min(r0 + kKvPromptRows, packed) - 1) / G;
-  const int w_first = uni(sq.start + min(r0 + wave * 32, packed - 1) / G);
-  const int w_last = uni(sq.start + min(r0 + wave * 32 + 31, packed - 1) / G);
+  const int pos = tile.start + t, lo = A.window ? max(0, pos - A.window + 1) : 0;
+  const int len = tile.start + tile.rows;
+  const int wg_first = tile.start + r0 / G, wg_last = tile.start + (min(r0 + kKvPromptRows, packed) - 1) / G;
+  const int w_first = uni(tile.start + min(r0 + wave * 32, packed - 1) / G);
+  const int w_last = uni(tile.start + min(r0 + wave * 32 + 31, packed - 1) / G);
   const int w_lo = A.window ? max(0, w_first - A.window + 1) : 0, w_all = A.window ? max(0, w_last - A.window + 1) : 0;
   half8 qf[KS];
   {
-    const _Float16* q = (const _Float16*)A.q + (int64_t)(sq.row0 + t) * A.q_stride + (head * G + rr % G) * D;
+    const _Float16* q = (const _Float16*)A.q + (int64_t)(tile.row0 + t) * A.q_stride + (head * G + rr % G) * D;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       qf[k] = *(const half8*)(q + k * 16 + h * 8);
@@ -889,7 +887,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
   const int g_lo = (A.window ? max(0, wg_first - A.window + 1) : 0) / kKvGroup, g_hi = wg_last / kKvGroup + 1;
   const int per = (g_hi - g_lo + tile.splits - 1) / tile.splits;
   const int g_begin = uni(g_lo + tile.split * per), g_end = uni(min(g_hi, g_begin + per));
-  const int32_t* row = kv_row(kv, sq.seq, A.layer, head);
+  const int32_t* row = kv_row(kv, tile.seq, A.layer, head);
   const int nb = kv.block / kKvGroup;
 
   uint4 kc[NU], vc[NU];
@@ -1049,7 +1047,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_k
       part[kKvRows * D + 2 * (n & 15) + 1] = l;
     }
   } else if (r < packed) {
-    _Float16* out = (_Float16*)A.out + (int64_t)(sq.row0 + t) * A.out_stride + (head * G + rr % G) * D;
+    _Float16* out = (_Float16*)A.out + (int64_t)(tile.row0 + t) * A.out_stride + (head * G + rr % G) * D;
     const float f = ref / Code<CODE>::kTop / l;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -1074,9 +1072,8 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
   const int tid = threadIdx.x, orow = blockIdx.x % kKvRows, at = blockIdx.x / kKvRows;
   const KvTile tile = A.combine[at / kv.n_kv];
   const int head = at % kv.n_kv;
-  const KvSeq sq = A.seqs[tile.s];
   const int G = kv.n_heads / kv.n_kv, gr = tile.tile * kKvRows + orow, side = tid / TR, d = tid % TR * 4;
-  if (gr >= sq.rows * G) return;
+  if (gr >= tile.rows * G) return;
   const int64_t step = kv.n_kv * kv_part_floats(D);
   const float* part = A.part + ((int64_t)tile.part * kv.n_kv + head) * kv_part_floats(D);
   float m = -FLT_MAX, l = 0.f;
@@ -1106,7 +1103,7 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
     ll += f * lds_l[s];
     o += f * *(const float4v*)&lds_o[s][d];
   }
-  T* out = (T*)A.out + (int64_t)(sq.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + d;
+  T* out = (T*)A.out + (int64_t)(tile.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + d;
   const float inv = 1.f / ll;
 #pragma unroll
   for (int j = 0; j < 4; ++j) out[j] = (T)(o[j] * inv);

@@ -99,10 +99,14 @@ struct slora_kv {
   }
 };
 
+// A sequence's part in a step: its id, the position of its first row, its rows
+// and the batch row of the first.
+struct StepSeq { int32_t seq, start, rows, row0; };
+
 struct slora_kv_step {
   slora_kv* kv = nullptr;
   bool reread = false;
-  std::vector<KvSeq> seqs;
+  std::vector<StepSeq> seqs;
   std::vector<uint64_t> gens;
   std::vector<int32_t> ends;       // blocks of each sequence at the end of the step
   std::vector<KvBlock> blocks;
@@ -115,8 +119,7 @@ struct slora_kv_step {
   const char* dev = nullptr;
 
   // byte offsets in the device metadata (every record is 16 bytes or more)
-  size_t blocks_off() const { return seqs.size() * sizeof(KvSeq); }
-  size_t prompts_off() const { return blocks_off() + blocks.size() * sizeof(KvBlock); }
+  size_t prompts_off() const { return blocks.size() * sizeof(KvBlock); }
   size_t tiles_off() const { return prompts_off() + prompts.size() * sizeof(KvTile); }
   size_t patches_off() const { return tiles_off() + (tiles.size() + combine.size()) * sizeof(KvTile); }
   size_t row_pos_off() const { return patches_off() + patches.size() * sizeof(KvPatch); }
@@ -144,14 +147,14 @@ void build_tiles(slora_kv_step* st) {
   const slora_kv_desc& d = st->kv->d;
   const int32_t G = d.n_heads / d.n_kv_heads;
   const bool half = st->kv->info.dtype == SLORA_F16;
-  auto prompt = [&](const KvSeq& s) { return half && (int64_t)s.rows * G >= kPromptMin; };
+  auto prompt = [&](const StepSeq& s) { return half && (int64_t)s.rows * G >= kPromptMin; };
   // key groups that the tile of packed rows [r0, r0 + n) sees, without a window
-  auto groups_of = [&](const KvSeq& s, int64_t r0, int64_t n) {
+  auto groups_of = [&](const StepSeq& s, int64_t r0, int64_t n) {
     return (s.start + (std::min<int64_t>(r0 + n, (int64_t)s.rows * G) - 1) / G) / kKvGroup + 1;
   };
   // groups of a workgroup: the fewest for which all row tiles' workgroups are at most kWantGroups
   std::vector<int64_t> lens;
-  for (const KvSeq& s : st->seqs)
+  for (const StepSeq& s : st->seqs)
     for (int64_t r0 = 0; !prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvRows) lens.push_back(groups_of(s, r0, kKvRows));
   int64_t chunk = kMinGroups;
   if (!lens.empty()) {
@@ -164,50 +167,49 @@ void build_tiles(slora_kv_step* st) {
       else chunk = mid + 1;
     }
   }
-  for (size_t i = 0; i < st->seqs.size(); ++i) {
-    const KvSeq& s = st->seqs[i];
+  // longest first
+  std::vector<std::pair<int64_t, KvTile>> found;
+  auto take = [&](std::vector<KvTile>* to) {
+    std::stable_sort(found.begin(), found.end(), [](const auto& a, const auto& b) { return a.first > b.first; });
+    for (const auto& t : found) to->push_back(t.second);
+    found.clear();
+  };
+  for (const StepSeq& s : st->seqs) {
     if (prompt(s)) continue;
-    const int64_t packed = (int64_t)s.rows * G;
-    for (int64_t t = 0; t * kKvRows < packed; ++t) {
-      const int64_t last = (std::min<int64_t>((t + 1) * kKvRows, packed) - 1) / G;   // token of the tile's last row
-      const int64_t groups = (s.start + last) / kKvGroup + 1;
+    for (int64_t t = 0; t * kKvRows < (int64_t)s.rows * G; ++t) {
+      const int64_t groups = groups_of(s, t * kKvRows, kKvRows);
       const int32_t splits = (int32_t)((groups + chunk - 1) / chunk);
-      KvTile tile{(int32_t)i, (int32_t)t, 0, splits, (int32_t)st->n_parts, {(int32_t)((groups + splits - 1) / splits), 0, 0}};
-      for (int32_t k = 0; k < splits; ++k) {
-        tile.split = k;
-        st->tiles.push_back(tile);
-      }
+      for (int32_t k = 0; k < splits; ++k)
+        found.push_back({(groups + splits - 1) / splits,
+                         {s.seq, (int32_t)t, k, splits, (int32_t)st->n_parts, s.start, s.rows, s.row0}});
       if (splits > 1) st->n_parts += splits;
     }
   }
+  take(&st->tiles);
   st->n_row_parts = st->n_parts;
+
   int64_t total = 0;
-  for (const KvSeq& s : st->seqs)
+  for (const StepSeq& s : st->seqs)
     for (int64_t r0 = 0; prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvPromptRows) total += groups_of(s, r0, kKvPromptRows);
   const int64_t most = std::max<int64_t>(kPromptGroups, (total * d.n_kv_heads + kWantPrompts - 1) / kWantPrompts);
-  for (size_t i = 0; i < st->seqs.size(); ++i) {
-    const KvSeq& s = st->seqs[i];
+  constexpr int32_t kRuns = kKvPromptRows / kKvRows;
+  for (const StepSeq& s : st->seqs) {
     const int64_t packed = (int64_t)s.rows * G;
     if (!prompt(s)) continue;
     for (int64_t t = 0; t * kKvPromptRows < packed; ++t) {
       const int64_t groups = groups_of(s, t * kKvPromptRows, kKvPromptRows);
       const int32_t splits = (int32_t)std::max<int64_t>(1, (groups + most / 2) / most);
-      KvTile tile{(int32_t)i, (int32_t)t, 0, splits, (int32_t)st->n_parts, {(int32_t)((groups + splits - 1) / splits), 0, 0}};
-      for (int32_t k = 0; k < splits; ++k) {
-        tile.split = k;
-        st->prompts.push_back(tile);
-      }
+      for (int32_t k = 0; k < splits; ++k)
+        found.push_back({(groups + splits - 1) / splits,
+                         {s.seq, (int32_t)t, k, splits, (int32_t)st->n_parts, s.start, s.rows, s.row0}});
       if (splits == 1) continue;
-      for (int32_t sub = 0; sub < kKvPromptRows / kKvRows; ++sub)
-        if (t * kKvPromptRows + sub * kKvRows < packed)
-          st->combine.push_back({(int32_t)i, (int32_t)(t * (kKvPromptRows / kKvRows)) + sub, 0, splits,
-                                 (int32_t)st->n_parts + sub * splits, {0, 0, 0}});
-      st->n_parts += (int64_t)splits * (kKvPromptRows / kKvRows);
+      for (int32_t run = 0; run < kRuns && t * kKvPromptRows + run * kKvRows < packed; ++run)
+        st->combine.push_back({s.seq, (int32_t)t * kRuns + run, 0, splits, (int32_t)st->n_parts + run * splits, s.start,
+                               s.rows, s.row0});
+      st->n_parts += (int64_t)splits * kRuns;
     }
   }
-  auto longer = [](const KvTile& a, const KvTile& b) { return a.pad[0] > b.pad[0]; };
-  std::stable_sort(st->prompts.begin(), st->prompts.end(), longer);
-  std::stable_sort(st->tiles.begin(), st->tiles.end(), longer);
+  take(&st->prompts);
 }
 
 slora_status check_launch(const std::string& f, const slora_kv* kv, const slora_kv_step* st, int32_t layer) {
@@ -443,8 +445,7 @@ slora_status slora_kv_step_upload(slora_kv_step* st, void* dev_meta, size_t dev_
     auto put = [&](size_t off, const void* src, size_t bytes) {
       if (bytes) std::memcpy(image.data() + off, src, bytes);
     };
-    put(0, st->seqs.data(), st->seqs.size() * sizeof(KvSeq));
-    put(st->blocks_off(), st->blocks.data(), st->blocks.size() * sizeof(KvBlock));
+    put(0, st->blocks.data(), st->blocks.size() * sizeof(KvBlock));
     put(st->prompts_off(), st->prompts.data(), st->prompts.size() * sizeof(KvTile));
     put(st->tiles_off(), st->tiles.data(), st->tiles.size() * sizeof(KvTile));
     put(st->tiles_off() + st->tiles.size() * sizeof(KvTile), st->combine.data(), st->combine.size() * sizeof(KvTile));
@@ -492,7 +493,7 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* st, int32_t laye
   if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
   KvAppend A{};
   A.kv = kv->view();
-  A.blocks = reinterpret_cast<const KvBlock*>(st->dev + st->blocks_off());
+  A.blocks = reinterpret_cast<const KvBlock*>(st->dev);
   A.n_blocks = (int32_t)st->blocks.size();
   A.n_small = st->n_small;
   A.n_rows = st->n_rows;
@@ -534,7 +535,6 @@ slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* st, int32_t laye
   if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
   KvAttend A{};
   A.kv = kv->view();
-  A.seqs = reinterpret_cast<const KvSeq*>(st->dev);
   A.tiles = reinterpret_cast<const KvTile*>(st->dev + st->tiles_off());
   A.prompts = reinterpret_cast<const KvTile*>(st->dev + st->prompts_off());
   A.n_prompts = (int32_t)st->prompts.size();
@@ -566,7 +566,7 @@ slora_status slora_kv_read(slora_kv* kv, const slora_kv_step* st, int32_t layer,
   if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
   KvRead R{};
   R.kv = kv->view();
-  R.blocks = reinterpret_cast<const KvBlock*>(st->dev + st->blocks_off());
+  R.blocks = reinterpret_cast<const KvBlock*>(st->dev);
   R.n_blocks = (int32_t)st->blocks.size();
   R.layer = layer;
   R.k = k;
