@@ -84,11 +84,11 @@ class KvStepInfo(ctypes.Structure):
 
 
 class KvCache(c_void_p):
-    """Handle of a cache; ``desc`` holds its description."""
+    """Handle of a cache; ``desc`` holds its description, ``heads`` its query and kv heads."""
 
 
 class KvStep(c_void_p):
-    """Handle of a step; ``kv`` is its cache and ``n_rows`` its rows."""
+    """Handle of a step; ``kv`` is its cache, ``n_rows`` its rows and ``dim`` the elements of a head."""
 
 
 _LIB = None
@@ -506,6 +506,7 @@ def slora_kv_create(pool, dev, dev_bytes: int, **desc) -> KvCache:
     kv.desc = KvDesc(**desc)
     _check(lib().slora_kv_create(pool, ctypes.byref(kv.desc), _ptr(dev), int(dev_bytes), ctypes.byref(kv)),
            "slora_kv_create")
+    kv.heads = (kv.desc.n_heads, kv.desc.n_kv_heads)
     return kv
 
 
@@ -538,7 +539,7 @@ def slora_kv_build_step(kv, seqs, counts, reread: bool = False) -> KvStep:
     _check(lib().slora_kv_build_step(kv, seqs.size, _i32p(seqs) if seqs.size else None,
                                      _i32p(counts) if seqs.size else None, int(reread), ctypes.byref(step)),
            "slora_kv_build_step")
-    step.kv, step.n_rows = kv, int(counts.sum(dtype=np.int64))
+    step.kv, step.n_rows, step.dim = kv, int(counts.sum(dtype=np.int64)), kv.desc.head_dim
     return step
 
 
@@ -560,44 +561,50 @@ def slora_kv_step_upload(step, dev_meta, dev_meta_bytes: int, stream=None) -> No
 def _rows(x, step, heads: int, stride):
     """(address, stride in elements between tokens) of a [n_rows, heads, head_dim] operand: a tensor of that shape
     whose heads are contiguous, or a raw address with its stride (contiguous by default)."""
-    dim = step.kv.desc.head_dim
     if x is None:
         return 0, 0
-    if hasattr(x, "stride") and hasattr(x, "shape"):
-        if tuple(x.shape[1:]) != (heads, dim) or x.shape[0] < step.n_rows:
-            raise ValueError(f"expected at least {step.n_rows} rows of {heads} heads of {dim}, got {tuple(x.shape)}")
-        if x.shape[0] and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim)):
-            raise ValueError("the heads of a row must be contiguous")
-        if stride is None and x.shape[0] > 1:
-            stride = x.stride(0)
-    return _ptr(x), heads * dim if stride is None else int(stride)
+    dim = step.dim
+    try:
+        n, h, d = x.shape
+        sn, sh, sd = x.stride()
+    except AttributeError:                               # a raw address
+        return _ptr(x), heads * dim if stride is None else int(stride)
+    if h != heads or d != dim or n < step.n_rows:
+        raise ValueError(f"expected at least {step.n_rows} rows of {heads} heads of {dim}, got {tuple(x.shape)}")
+    if n and (sd != 1 or (sh != dim and heads > 1)):
+        raise ValueError("the heads of a row must be contiguous")
+    if stride is None:
+        stride = sn if n > 1 else heads * dim
+    return x.data_ptr(), stride
 
 
 def slora_kv_append(kv, step, layer: int, k, v, q=None, q_out=None, cos_sin=None, stream=None, k_stride=None,
                     v_stride=None, q_stride=None, q_out_stride=None, n_positions=None) -> None:
     """cos_sin: a contiguous fp32 tensor [n_positions, rot_dim], or a raw address with n_positions."""
-    d = kv.desc
+    heads, kv_heads = kv.heads
     if cos_sin is not None and n_positions is None:
-        if cos_sin.dim() != 2 or cos_sin.shape[1] != d.rot_dim or not cos_sin.is_contiguous():
+        if cos_sin.dim() != 2 or cos_sin.shape[1] != kv.desc.rot_dim or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous [n_positions, rot_dim] tensor")
         n_positions = cos_sin.shape[0]
-    qp, qs = _rows(q, step, d.n_heads, q_stride)
-    op, os_ = _rows(q_out, step, d.n_heads, q_out_stride)
-    kp, ks = _rows(k, step, d.n_kv_heads, k_stride)
-    vp, vs = _rows(v, step, d.n_kv_heads, v_stride)
+    qp, qs = _rows(q, step, heads, q_stride)
+    op, os_ = _rows(q_out, step, heads, q_out_stride)
+    kp, ks = _rows(k, step, kv_heads, k_stride)
+    vp, vs = _rows(v, step, kv_heads, v_stride)
     _check(lib().slora_kv_append(kv, step, layer, qp, qs, op, os_, kp, ks, vp, vs, _ptr(cos_sin), n_positions or 0,
                                  _stream(stream)), "slora_kv_append")
 
 
 def slora_kv_attend(kv, step, layer: int, q, out, scale: float, window: int = 0, workspace=None,
                     workspace_bytes: int = 0, stream=None, q_stride=None, out_stride=None) -> None:
-    qp, qs = _rows(q, step, kv.desc.n_heads, q_stride)
-    op, os_ = _rows(out, step, kv.desc.n_heads, out_stride)
+    heads = kv.heads[0]
+    qp, qs = _rows(q, step, heads, q_stride)
+    op, os_ = _rows(out, step, heads, out_stride)
     _check(lib().slora_kv_attend(kv, step, layer, qp, qs, op, os_, scale, window, _ptr(workspace),
                                  int(workspace_bytes), _stream(stream)), "slora_kv_attend")
 
 
 def slora_kv_read(kv, step, layer: int, k=None, v=None, stream=None, k_stride=None, v_stride=None) -> None:
-    kp, ks = _rows(k, step, kv.desc.n_kv_heads, k_stride)
-    vp, vs = _rows(v, step, kv.desc.n_kv_heads, v_stride)
+    kv_heads = kv.heads[1]
+    kp, ks = _rows(k, step, kv_heads, k_stride)
+    vp, vs = _rows(v, step, kv_heads, v_stride)
     _check(lib().slora_kv_read(kv, step, layer, kp, ks, vp, vs, _stream(stream)), "slora_kv_read")
