@@ -11,6 +11,7 @@ namespace slora {
 
 constexpr int kKvGroup = 32;      // tokens of one attention step: block_tokens is a multiple
 constexpr int kKvRows = 16;       // query rows of one row tile
+constexpr int kKvCus = 256;       // compute units of an MI355X
 constexpr int kKvPromptRows = 128;   // query rows of one prompt tile
 
 // Page layout (one block of one kv head): the K codes, then the V codes, both

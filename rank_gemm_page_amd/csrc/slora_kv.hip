@@ -855,8 +855,7 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
 
 // ---------------------------------------------------------------------------
 // Attention of a long run of rows (prompts), fp16: 128 packed rows of one kv
-// head a workgroup, 32 a wave, over keys staged 64 at a time (32 for heads of
-// 256).  The codes of the next keys are loaded while these are multiplied, then
+// head a workgroup, 32 a wave, over keys staged 32 or 64 at a time.  The codes of the next keys are loaded while these are multiplied, then
 // converted once for all four waves into fp16 in LDS, two buffers in turn.
 //
 // The 32x32x16 instruction as in the row tiles: S^T = K Q^T leaves lane (h, n) =
@@ -879,9 +878,9 @@ __device__ __forceinline__ int v_slot(int d, int t, int h) {
   return p * 8 + (((d & 1) * 4 + 2 * t + h) ^ ((p >> 1 & 1) | (p >> 2 & 2) | (p & 4)));
 }
 
-template <int CODE, int D>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_attend_prompt_kernel(KvAttend A) {
-  constexpr int NG = D == 256 ? 1 : 2;           // groups of 32 keys staged at a time
+template <int CODE, int D, bool TRIPLE>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_attend_prompt_kernel(KvAttend A) {
+  constexpr int NG = D == 256 || TRIPLE ? 1 : 2; // groups of 32 keys staged at a time
   constexpr int KS = D / 16, NB = D / 32;        // steps of the K product, blocks of 32 elements
   constexpr int UG = 2 * D, NU = NG * UG / kThreads;   // 16-byte units of a group (of K, of V) and of a thread
   __shared__ uint4 lds_k[2][NG][32 * D / 8];
@@ -1254,9 +1253,10 @@ static const void* rows_of(int code, int dim) {
   return code == SLORA_KV_INT8 ? rows_of<T, SLORA_KV_INT8>(dim) : rows_of<T, SLORA_KV_FP8>(dim);
 }
 template <int CODE>
-static const void* prompt_of(int dim) {
-  return dim == 64 ? (const void*)kv_attend_prompt_kernel<CODE, 64>
-         : dim == 128 ? (const void*)kv_attend_prompt_kernel<CODE, 128> : (const void*)kv_attend_prompt_kernel<CODE, 256>;
+static const void* prompt_of(int dim, bool triple) {
+  return dim == 64 ? (const void*)kv_attend_prompt_kernel<CODE, 64, false>
+         : dim == 256 ? (const void*)kv_attend_prompt_kernel<CODE, 256, false>
+         : triple ? (const void*)kv_attend_prompt_kernel<CODE, 128, true> : (const void*)kv_attend_prompt_kernel<CODE, 128, false>;
 }
 template <typename T>
 static const void* combine_of(int dim) {
@@ -1280,8 +1280,15 @@ hipError_t launch_kv_append(const KvAppend& A0, hipStream_t stream) {
 
 hipError_t launch_kv_attend(const KvAttend& A, hipStream_t stream) {
   const bool half = A.kv.dtype == SLORA_F16;
-  hipError_t e = run(A.kv.code == SLORA_KV_INT8 ? prompt_of<SLORA_KV_INT8>(A.kv.dim) : prompt_of<SLORA_KV_FP8>(A.kv.dim),
-                     (int64_t)A.n_prompts * A.kv.n_kv, A, stream);
+  // Three workgroups a CU (32 keys staged at a time) hide each other's staging
+  // better than two with 64: prompts of 512 tokens 149 against 157 us, of 4096
+  // 668 against 700 us.  But four of about the same length on every CU leave the
+  // last one alone on it (612 against 560 us): those run two and two.
+  const int64_t prompts = (int64_t)A.n_prompts * A.kv.n_kv;
+  const bool triple = (prompts + kKvCus - 1) / kKvCus != 4;
+  hipError_t e = run(A.kv.code == SLORA_KV_INT8 ? prompt_of<SLORA_KV_INT8>(A.kv.dim, triple)
+                                                : prompt_of<SLORA_KV_FP8>(A.kv.dim, triple),
+                     prompts, A, stream);
   if (e != hipSuccess) return e;
   e = run(half ? rows_of<_Float16>(A.kv.code, A.kv.dim) : rows_of<float>(A.kv.code, A.kv.dim),
                      (int64_t)A.n_tiles * A.kv.n_kv, A, stream);

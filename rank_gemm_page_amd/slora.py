@@ -84,7 +84,8 @@ class KvStepInfo(ctypes.Structure):
 
 
 class KvCache(c_void_p):
-    """Handle of a cache; ``desc`` holds its description, ``heads`` its query and kv heads."""
+    """Handle of a cache; ``desc`` holds its description, ``heads`` its query and kv heads, ``rot`` its rotated
+    elements."""
 
 
 class KvStep(c_void_p):
@@ -506,7 +507,7 @@ def slora_kv_create(pool, dev, dev_bytes: int, **desc) -> KvCache:
     kv.desc = KvDesc(**desc)
     _check(lib().slora_kv_create(pool, ctypes.byref(kv.desc), _ptr(dev), int(dev_bytes), ctypes.byref(kv)),
            "slora_kv_create")
-    kv.heads = (kv.desc.n_heads, kv.desc.n_kv_heads)
+    kv.heads, kv.rot = (kv.desc.n_heads, kv.desc.n_kv_heads), kv.desc.rot_dim
     return kv
 
 
@@ -583,7 +584,7 @@ def slora_kv_append(kv, step, layer: int, k, v, q=None, q_out=None, cos_sin=None
     """cos_sin: a contiguous fp32 tensor [n_positions, rot_dim], or a raw address with n_positions."""
     heads, kv_heads = kv.heads
     if cos_sin is not None and n_positions is None:
-        if cos_sin.dim() != 2 or cos_sin.shape[1] != kv.desc.rot_dim or not cos_sin.is_contiguous():
+        if cos_sin.dim() != 2 or cos_sin.shape[1] != kv.rot or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous [n_positions, rot_dim] tensor")
         n_positions = cos_sin.shape[0]
     qp, qs = _rows(q, step, heads, q_stride)
