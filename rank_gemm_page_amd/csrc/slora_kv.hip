@@ -855,8 +855,9 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
 
 // ---------------------------------------------------------------------------
 // Attention of a long run of rows (prompts), fp16: 128 packed rows of one kv
-// head a workgroup, 32 a wave, over keys staged 32 or 64 at a time.  The codes of the next keys are loaded while these are multiplied, then
-// converted once for all four waves into fp16 in LDS, two buffers in turn.
+// head a workgroup, 32 a wave, over keys staged 32 or 64 at a time.  The codes
+// of the next keys are loaded while these are multiplied, then converted once
+// for all four waves into fp16 in LDS, two buffers in turn.
 //
 // The 32x32x16 instruction as in the row tiles: S^T = K Q^T leaves lane (h, n) =
 // 32 h + n with query row n and keys 8a + 4h + b (a, b = 0 .. 3), registers 4a +
@@ -898,6 +899,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
   const int wg_first = tile.start + r0 / G, wg_last = tile.start + (min(r0 + kKvPromptRows, packed) - 1) / G;
   const int w_first = uni(tile.start + min(r0 + wave * 32, packed - 1) / G);
   const int w_last = uni(tile.start + min(r0 + wave * 32 + 31, packed - 1) / G);
+  // a wave without rows only stages (asked for in the two-workgroup form, the
+  // loop came out 12 % slower, where such waves are rare)
+  const bool idle = r0 + wave * 32 >= packed;
   const int w_lo = A.window ? max(0, w_first - A.window + 1) : 0, w_all = A.window ? max(0, w_last - A.window + 1) : 0;
   half8 qf[KS];
   {
@@ -984,7 +988,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
 #pragma unroll
     for (int x = 0; x < NG; ++x) {
       const int key0 = (gb + x) * kKvGroup;
-      if (gb + x >= g_end || key0 > w_last || key0 + kKvGroup <= w_lo) continue;
+      if (gb + x >= g_end || key0 > w_last || key0 + kKvGroup <= w_lo || (TRIPLE && idle)) continue;
       float16v s = {};
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -1139,7 +1143,9 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
 // elements of a token from K, and a 16-byte unit of V, turned across four lanes
 // into 8 elements of each of two tokens, so that stores are 16 bytes a lane and
 // 64 bytes or more a run.  Nothing here reads them again: non-temporal stores
-// took 8 sequences of up to 4000 tokens from 22.0 to 18.2 us (4.0 to 5.1 TB/s).
+// took 8 sequences of up to 4000 tokens from 22.0 to 18.2 us (5.1 TB/s).  fp32
+// rows are stored in two halves of every 32 bytes, which such stores do not
+// merge (3.2 TB/s against 4.6).
 
 template <typename T, int CODE>
 __device__ __forceinline__ void put8(T* p, uint32_t a, uint32_t b, float unit) {
@@ -1149,7 +1155,8 @@ __device__ __forceinline__ void put8(T* p, uint32_t a, uint32_t b, float unit) {
     y[j] = (T)(Code<CODE>::value((a >> (8 * j)) & 0xFF) * unit);
     y[4 + j] = (T)(Code<CODE>::value((b >> (8 * j)) & 0xFF) * unit);
   }
-  __builtin_nontemporal_store(y, reinterpret_cast<typename Vec<T>::v8*>(p));
+  if (sizeof(T) == 2) __builtin_nontemporal_store(y, reinterpret_cast<typename Vec<T>::v8*>(p));
+  else *reinterpret_cast<typename Vec<T>::v8*>(p) = y;
 }
 
 template <typename T, int CODE>

@@ -130,16 +130,19 @@ struct slora_kv_step {
 
 namespace {
 
-// Key groups of 32 a workgroup takes at least, and the workgroups a launch
-// aims at: below the first a split costs more than it brings, and above the
-// second the chip is full several times over.
+// Row tiles: key groups of 32 a workgroup takes at least, and the workgroups a
+// launch is split into at most.  Fewer than 8 groups bring nothing (one token
+// after 777: 10 us with 4, 8 and 16); 2048 workgroups fill the places of the
+// chip, two a CU for heads of 128, four times.
 constexpr int64_t kMinGroups = 8, kWantGroups = 2048;
 
-// Sequences with at least this many packed rows (query heads of a kv head times
-// rows) take the prompt tiles (fp16), whose keys are split only where a launch
-// has fewer tiles than the chip holds twice over: a workgroup takes at least
-// kPromptGroups groups.
-constexpr int64_t kPromptMin = 64, kPromptGroups = 16, kWantPrompts = 1024;
+// Sequences with at least kPromptMin packed rows (query heads of a kv head times
+// rows) take the prompt tiles (fp16).  Around there: 50 rows after 2000 tokens
+// 134 us in them against 152 in row tiles, 56 rows after 1000 tokens 49 in both,
+// 40 after 1000 tokens 47 against 39.  Their keys are split only where a launch
+// has fewer tiles than kWantPrompts, the chip's places over: a workgroup takes
+// at least kPromptGroups groups.
+constexpr int64_t kPromptMin = 48, kPromptGroups = 16, kWantPrompts = 1024;
 
 // Tiles of 128 packed rows for long runs of rows (fp16), and row tiles of 16 for
 // the others, with their key splits, longest first.
