@@ -369,11 +369,13 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
                               return b.slot1 - b.slot0 == 1;
                             }) - st->blocks.begin());
     build_tiles(st);
-    // every workgroup index of a launch is 31 bits
-    const int64_t most = std::max({2 * (int64_t)st->blocks.size(), (int64_t)st->tiles.size(), (int64_t)st->combine.size() * kKvRows, st->n_parts}) *
-                             kv->d.n_kv_heads +
-                         rows * kv->d.n_heads * kv->d.head_dim / 16 / kThreads;
-    if (most > INT32_MAX / 2 || rows * kv->d.n_heads > INT32_MAX / 2 || patches > INT32_MAX / 2) {
+    // a launch holds fewer than 2^32 threads
+    constexpr int64_t kMostGroups = ((int64_t)1 << 32) / kThreads - 1;
+    const int64_t kvh = kv->d.n_kv_heads;
+    const int64_t append = 2 * (int64_t)st->blocks.size() * kvh + (rows * kv->d.n_heads * (kv->d.head_dim / 16)) / kThreads + 1;
+    if (std::max({append, (int64_t)st->prompts.size() * kvh, (int64_t)st->tiles.size() * kvh,
+                  (int64_t)st->combine.size() * kvh * kKvRows, patches / kThreads}) > kMostGroups ||
+        rows * kv->d.n_heads > INT32_MAX / 2 || st->n_parts * kvh > INT32_MAX / 2) {
       delete st;
       return fail(SLORA_E_INVAL, "slora_kv_build_step: the step is too large for one launch");
     }
@@ -383,7 +385,11 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
     }
     std::vector<int32_t> ids((size_t)need);
     st->patches.reserve((size_t)patches);
-    for (int32_t i = 0; i < n; ++i) kv->seqs[seqs[i]].pages.reserve((size_t)(st->ends[i] * kv->per_block()));
+    for (int32_t i = 0; i < n; ++i) {
+      std::vector<int32_t>& pages = kv->seqs[seqs[i]].pages;
+      const size_t want = (size_t)(st->ends[i] * kv->per_block());
+      if (want > pages.capacity()) pages.reserve(std::max(want, 2 * pages.capacity()));
+    }
     slora_status got = slora_alloc_pages(kv->pool, kv->d.cls, need, ids.data());
     if (got != SLORA_OK) {
       delete st;

@@ -80,26 +80,93 @@ def test_long_sequences_split_their_keys(dtype, code, length, rows):
 
 
 @pytest.mark.parametrize("code", CODES)
-def test_peaked_and_far_apart_scores(code):
-    """Scores of some hundreds: nearly all weight on one key, references raised again and again."""
+@pytest.mark.parametrize("rows", [3, 70])
+def test_peaked_and_far_apart_scores(code, rows):
+    """Scores of some hundreds: nearly all weight on one key, references raised again and again; scales of both signs
+    and none (70 rows take the prompt tiles)."""
     with KvCase(torch, "f16", code, 4, 4, 64, 32) as c:
         c.append([0], [200], 6.0)
-        st, info, ws, q, starts = c.append([0], [3], 6.0, q=c.draw(3, 4) * np.float16(6))
+        st, info, ws, q, starts = c.append([0], [rows], 6.0, q=c.draw(rows, 4) * np.float16(6))
         for scale in (1.0, -0.5, 0.0):
             out = c.attend(st, q, ws, scale)
-            c.check_attend(out, q, [0], [3], starts, scale)
+            c.check_attend(out, q, [0], [rows], starts, scale)
 
 
 @pytest.mark.parametrize("code", CODES)
-def test_block_ranges_of_very_different_size(code):
-    """Value ranges that fall and rise by thousands from block to block, and blocks of zeros."""
-    with KvCase(torch, "f16", code, 2, 2, 64, 32) as c:
+@pytest.mark.parametrize("heads,dim", [(2, 64), (8, 64), (8, 128), (4, 256)])
+def test_block_ranges_of_very_different_size(code, heads, dim):
+    """Value ranges that fall and rise by thousands from block to block, and blocks of zeros, in row tiles (2 heads)
+    and prompt tiles."""
+    with KvCase(torch, "f16", code, heads, 2, dim, 32) as c:
         for gain in (1.0, 2e-4, 3e3, 0.0, 1e-3, 50.0, 0.0):
             v = (c.draw(32, 2).astype(np.float32) * gain).astype(np.float16)
             st, info, ws, q, starts = c.append([0], [32], v=v)
             out = c.attend(st, q, ws, 0.125)
             c.check_attend(out, q, [0], [32], starts, 0.125)
         c.check_read([0])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("rows", [2, 40])
+def test_a_row_of_nan_is_alone(dtype, rows):
+    """A query row of NaN or infinity gives NaN there and changes no other row (split keys included)."""
+    with KvCase(torch, dtype, 0, 4, 2, 64, 32, max_tokens=1200) as c:
+        c.append([0, 1], [1000, 3])
+        st, info, ws, q, starts = c.append([0, 1], [rows, 1])
+        clean = c.attend(st, q, ws, 0.125)
+        for bad in (float("nan"), float("inf")):
+            x = q.clone()
+            x[1, 2, 7] = bad
+            out = c.attend(st, x, ws, 0.125)
+            assert torch.isnan(out[1, 2]).all()
+            out[1, 2] = clean[1, 2]
+            assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("dim,tokens", [(128, 224), (64, 448), (256, 96)])
+def test_blocks_of_the_second_page_class(dim, tokens):
+    """A pool of two classes with the blocks in the larger pages: 224 tokens and more a block."""
+    n = 40
+    mem = [torch.full((n, 1024), 255, dtype=torch.uint8, device="cuda:0"),
+           torch.full((n, 57344), 255, dtype=torch.uint8, device="cuda:0")]
+    pool = S.slora_pool_create(S.SLORA_F16, 512, 28672, 1, 1, 1, mem, [n, n])
+    desc = dict(cls=1, code=S.SLORA_KV_FP8, n_layers=1, n_heads=4, n_kv_heads=2, head_dim=dim,
+                block_tokens=0 if dim != 256 else 96, max_seqs=2, max_tokens=900, rot_dim=dim)
+    dev = torch.empty(S.slora_kv_device_bytes(pool, **desc), dtype=torch.uint8, device="cuda:0")
+    kv = S.slora_kv_create(pool, dev, dev.numel(), **desc)
+    cs = O.angles(900, dim)
+    model, rng = O.KvModel(S.SLORA_KV_FP8, 4, 2, dim, tokens, dim, O.HALVES, cs), np.random.default_rng(1)
+    cos_sin, steps, keep = torch.from_numpy(cs).to("cuda:0"), [], []
+    try:
+        for count in (1, 500, 1, 130, 30):
+            st = S.slora_kv_build_step(kv, [1], [count])
+            steps.append(st)
+            info = S.slora_kv_step_get_info(st)
+            meta, ws = (torch.empty(max(16, info[k]), dtype=torch.uint8, device="cuda:0")
+                        for k in ("meta_bytes", "workspace_bytes"))
+            keep += [meta, ws]
+            S.slora_kv_step_upload(st, meta, meta.numel(), torch.cuda.current_stream())
+            start = model.length(1)
+            q, k, v = (rng.standard_normal((count, h, dim)).astype(np.float16) for h in (4, 2, 2))
+            model.append(1, 0, k, v)
+            dq, dk, dv = (torch.from_numpy(x).to("cuda:0") for x in (q, k, v))
+            out = torch.empty_like(dq)
+            S.slora_kv_append(kv, st, 0, dk, dv, dq, dq, cos_sin=cos_sin, stream=torch.cuda.current_stream())
+            S.slora_kv_attend(kv, st, 0, dq, out, 0.1, 0, ws, ws.numel(), torch.cuda.current_stream())
+            S.slora_kv_read(kv, st, 0, dk, dv, torch.cuda.current_stream())
+            want, weight, *_ = model.attend(1, 0, dq.cpu().numpy(), start, 0.1)
+            # a weight and the output are rounded to fp16 once each, everything else to fp32 or better
+            assert (np.abs(out.cpu().numpy() - want) <= weight * 2.0 ** -10 + 2.0 ** -11 * np.abs(want) + 2.0 ** -24).all()
+            for what, x in ((0, dk), (1, dv)):
+                value = model.values(1, 0, what, start)
+                assert (np.abs(x.cpu().numpy() - value) <= 2.0 ** -10 * np.abs(value) + 2.0 ** -24).all()
+        assert len(S.slora_kv_pages(kv, 1)) == -(-662 // tokens)
+    finally:
+        torch.cuda.synchronize()
+        for st in steps:
+            S.slora_kv_step_destroy(st)
+        S.slora_kv_destroy(kv)
+        S.slora_pool_destroy(pool)
 
 
 @pytest.mark.parametrize("dtype,code", itertools.product(["f16", "f32"], CODES))

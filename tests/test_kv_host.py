@@ -128,6 +128,13 @@ def test_bad_steps_are_refused():
         refused(S.SLORA_E_INVAL, S.slora_kv_drop, c.kv, 3)
 
 
+def test_a_step_too_large_for_a_launch_is_refused():
+    with Cache(n_pages=1 << 20, n_layers=1, n_heads=64, n_kv_heads=64, max_seqs=1, max_tokens=1 << 26) as c:
+        msg = refused(S.SLORA_E_INVAL, S.slora_kv_build_step, c.kv, [0], [1 << 24])
+        assert "too large" in msg and S.slora_kv_length(c.kv, 0) == 0
+        assert S.slora_free_count(c.pool, 0) == 1 << 20
+
+
 def test_drop_returns_pages_and_makes_steps_stale():
     with Cache() as c:
         s = c.step([0, 1], [40, 40])
