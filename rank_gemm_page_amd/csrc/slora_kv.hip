@@ -530,6 +530,11 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
 // the second operand of O^T += V^T P^T without leaving their registers.  The
 // four waves of a workgroup take consecutive quarters of the keys and join
 // through LDS at the end.
+//
+// Of 16 rows a single token fills only G; the matrix cores have ten times what
+// HBM can feed that way, and a vector dot product would spend its instructions
+// on the conversions alone.  256 requests of 300 to 2000 tokens, 32 heads: 370 us,
+// 6.2 TB/s of codes (the largest copy runs at 5.2, reads alone at up to 6.6).
 
 template <typename T> struct Frag;
 template <> struct Frag<_Float16> { typedef half8 type; };
