@@ -369,13 +369,13 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
                               return b.slot1 - b.slot0 == 1;
                             }) - st->blocks.begin());
     build_tiles(st);
-    // a launch holds fewer than 2^32 threads (and a step no more page table entries than that has workgroups)
+    // a launch holds fewer than 2^32 threads, and counts in the kernels are 31 bits
     constexpr int64_t kMostGroups = ((int64_t)1 << 32) / kThreads - 1;
     const int64_t kvh = kv->d.n_kv_heads;
     const int64_t append = 2 * (int64_t)st->blocks.size() * kvh + (rows * kv->d.n_heads * (kv->d.head_dim / 16)) / kThreads + 1;
     if (std::max({append, (int64_t)st->prompts.size() * kvh, (int64_t)st->tiles.size() * kvh,
-                  (int64_t)st->combine.size() * kvh * kKvRows, patches}) > kMostGroups ||
-        rows * kv->d.n_heads > INT32_MAX / 2 || st->n_parts * kvh > INT32_MAX / 2) {
+                  (int64_t)st->combine.size() * kvh * kKvRows}) > kMostGroups ||
+        patches > INT32_MAX / 2 || rows * kv->d.n_heads > INT32_MAX / 2 || st->n_parts * kvh > INT32_MAX / 2) {
       delete st;
       return fail(SLORA_E_INVAL, "slora_kv_build_step: the step is too large for one launch");
     }
