@@ -533,8 +533,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
 //
 // Of 16 rows a single token fills only G; the matrix cores have ten times what
 // HBM can feed that way, and a vector dot product would spend its instructions
-// on the conversions alone.  256 requests of 300 to 2000 tokens, 32 heads: 370 us,
-// 6.2 TB/s of codes (the largest copy runs at 5.2, reads alone at up to 6.6).
+// on the conversions alone.  256 requests of 300 to 2000 tokens, 32 heads: 350 us,
+// 6.5 TB/s of codes (the largest copy runs at 5.2, reads alone at up to 6.6).
 
 template <typename T> struct Frag;
 template <> struct Frag<_Float16> { typedef half8 type; };
@@ -603,8 +603,12 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, int splits, uint32_t*
   return *lds == (uint32_t)splits - 1;
 }
 
+// The bound of two waves a SIMD makes the compiler spare registers: three run at
+// heads of 128 (147 registers instead of 184, decode batch 374 to 350 us) and five
+// at 64.  Heads of 256 reach two by loading the next keys only when these are
+// multiplied (f16 324 to 194 registers, 9000 tokens on 4 kv heads 88 to 61 us).
 template <typename T, int CODE, int D>
-__global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
+__global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A) {
   using F = typename Frag<T>::type;
   constexpr int NC = D / 64, NE = D / 32, NT = D / 16;
   constexpr int DC = D < 128 ? D : 128;          // columns joined at a time
@@ -660,8 +664,7 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
     const char* kb = kv.base + (int64_t)page * kv.page_bytes + (int64_t)sub * kKvGroup * D;
     const char* vb = kb + (int64_t)kv.block * D;
     // With one tile a sequence its keys are read once: loads that leave the
-    // caches alone took the 256-request decode batch from 394 to 355 us (5.8 to
-    // 6.4 TB/s).  Further tiles find them in the caches.
+    // caches alone took the 256-request decode batch from 394 to 355 us.  Further tiles find them in the caches.
     if (once) {
 #pragma unroll
       for (int n = 0; n < 2 * NC; ++n) kx[n] = ld16_once(kb + n * 1024 + i * 64 + g * 16);
@@ -681,7 +684,7 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
   for (; gi < ge; ++gi) {
     uint4 kn[2 * NC], vn[NE];
     float rkn = 0.f, rvn = 0.f;
-    if (gi + 1 < ge) load(kn, vn, rkn, rvn);
+    if (D < 256 && gi + 1 < ge) load(kn, vn, rkn, rvn);
     const int key0 = gi * kKvGroup;
 
     float4v s0 = {0.f, 0.f, 0.f, 0.f}, s1 = {0.f, 0.f, 0.f, 0.f};
@@ -763,7 +766,7 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
     if (rv != rv && seen) l = __uint_as_float(0x7FC00000u);
     // fp16: each weight as the sum of two, so that the output's rounding is all
     // that shows (with one, the error against 64 bits was up to 1.4 times that);
-    // the second product costs 3 % of a decode batch
+    // the second product cost 3 % of a decode batch
     const F pf = frag8(p, (F*)nullptr);
     float rest[8];
 #pragma unroll
@@ -778,6 +781,10 @@ __global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttend A) {
       codes8<CODE>(vf[e].z, vf[e].w, &a);
       acc[2 * e + 1] = mma(a, pf, acc[2 * e + 1]);
       if (sizeof(T) == 2) acc[2 * e + 1] = mma(a, pr, acc[2 * e + 1]);
+    }
+    if (D == 256) {
+      if (gi + 1 < ge) load(kf, vf, rk, rv);
+      continue;
     }
 #pragma unroll
     for (int n = 0; n < 2 * NC; ++n) kf[n] = kn[n];

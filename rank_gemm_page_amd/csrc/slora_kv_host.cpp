@@ -132,9 +132,10 @@ namespace {
 
 // Row tiles: key groups of 32 a workgroup takes at least, and the workgroups a
 // launch is split into at most.  Fewer than 8 groups bring nothing (one token
-// after 777: 10 us with 4, 8 and 16); 2048 workgroups fill the places of the
-// chip, two a CU for heads of 128, four times.
-constexpr int64_t kMinGroups = 8, kWantGroups = 2048;
+// after 777: 10 us with 4, 8 and 16); 1536 workgroups fill the places of the
+// chip, three a CU for heads of 128, twice (12 long conversations: 108 us, 110
+// with 2048, 120 with 3840).
+constexpr int64_t kMinGroups = 8, kWantGroups = 1536;
 
 // Sequences with at least kPromptMin packed rows (query heads of a kv head times
 // rows) take the prompt tiles (fp16).  Around there: 50 rows after 2000 tokens
