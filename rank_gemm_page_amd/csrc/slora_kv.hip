@@ -905,8 +905,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
   const int G = kv.n_heads / kv.n_kv, packed = tile.rows * G, r0 = tile.tile * kKvPromptRows;
 
   // this lane's query row; rows past the last one repeat it and are not stored
-  const int r = r0 + wave * 32 + n, rr = min(r, packed - 1), t = rr / G;
-  const int pos = tile.start + t, lo = A.window ? max(0, pos - A.window + 1) : 0;
+  const int r = r0 + wave * 32 + n, rr = min(r, packed - 1);
+  int pos = tile.start + rr / G;
+  asm("" : "+v"(pos));                           // all that is kept of its row: the rest would be spilled
+  const uint32_t window = A.window ? (uint32_t)A.window : 1u << 31;
   const int len = tile.start + tile.rows;
   const int wg_first = tile.start + r0 / G, wg_last = tile.start + (min(r0 + kKvPromptRows, packed) - 1) / G;
   const int w_first = uni(tile.start + min(r0 + wave * 32, packed - 1) / G);
@@ -917,7 +919,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
   const int w_lo = A.window ? max(0, w_first - A.window + 1) : 0, w_all = A.window ? max(0, w_last - A.window + 1) : 0;
   half8 qf[KS];
   {
-    const _Float16* q = (const _Float16*)A.q + (int64_t)(tile.row0 + t) * A.q_stride + (head * G + rr % G) * D;
+    const _Float16* q = (const _Float16*)A.q + (int64_t)(tile.row0 + pos - tile.start) * A.q_stride + (head * G + rr % G) * D;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       qf[k] = *(const half8*)(q + k * 16 + h * 8);
@@ -985,7 +987,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
   float16v acc[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) acc[b] = float16v{};
-  float m = -FLT_MAX, l = 0.f, ref = 0.f;
+  float m = -FLT_MAX, l = 0.f, ref = 0.f, minus = -1.f;
+  asm("" : "+s"(minus));
   const int vd = (n >> 2 & 1) * 16 + (n >> 3) * 4 + (n & 3);     // element of this lane's row of a block of V^T
 
   if (g_begin < g_end) {
@@ -1016,7 +1019,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int key = key0 + (j >> 2) * 8 + h * 4 + (j & 3);
-          const bool in = key <= pos && key >= lo;
+          const bool in = (uint32_t)(pos - key) < window;      // key <= pos and key > pos - window
           s[j] = in ? s[j] : -INFINITY;
           seen |= in;
         }
@@ -1026,7 +1029,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
       for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
       top *= ck;
       if (__any(top > m + kLazy)) {
-        const float mn = fmaxf(m, fmaxf(top, __shfl_xor(top, 32))), f = __builtin_amdgcn_exp2f(m - mn);
+        // both halves of the wave, without an address register as a shuffle takes
+        const auto two = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+        const float mn = fmaxf(m, fmaxf(__uint_as_float(two[0]), __uint_as_float(two[1])));
+        const float f = __builtin_amdgcn_exp2f(m - mn);
         m = mn;
         l *= f;
 #pragma unroll
@@ -1047,23 +1053,36 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
         }
       }
       const float shift = __builtin_amdgcn_logf(unit) - m;
+      // each weight as the sum of two fp16 numbers, as in the row tiles: with one,
+      // the error against 64 bits was 1.1 to 1.35 times that of the output's own
+      // rounding.  The rest of a weight is one mixed-precision fma, for which the
+      // factor -1 must not look like a constant.
       float sum = 0.f;
-      half8 p[2];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], ck, shift));
-        sum += e;
-        p[j >> 3][j & 7] = (_Float16)e;
+      for (int tt = 0; tt < 2; ++tt) {
+        half8 p, rest;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * tt + j], ck, shift));
+          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * tt + j + 1], ck, shift));
+          sum += e0;
+          sum += e1;
+          const half2v two = __builtin_convertvector(float2v{e0, e1}, half2v);
+          p[j] = two[0];
+          p[j + 1] = two[1];
+          rest[j] = (_Float16)__builtin_fmaf((float)two[0], minus, e0);
+          rest[j + 1] = (_Float16)__builtin_fmaf((float)two[1], minus, e1);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const half8 a = __builtin_bit_cast(half8, lds_v[buf][x][v_slot(b * 32 + vd, tt, h)]);
+          acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, p, acc[b], 0, 0, 0);
+          acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, rest, acc[b], 0, 0, 0);
+        }
       }
       l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(unit), l);
       // a block whose range is NaN holds zero codes; the rows that see it are NaN
       if ((rk[x] != rk[x] || rv[x] != rv[x]) && seen) l = __uint_as_float(0x7FC00000u);
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-          acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              __builtin_bit_cast(half8, lds_v[buf][x][v_slot(b * 32 + vd, tt, h)]), p[tt], acc[b], 0, 0, 0);
     }
     if (more) {
       stage(buf ^ 1, gb + NG);
@@ -1088,7 +1107,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
       part[kKvRows * D + 2 * (n & 15) + 1] = l;
     }
   } else if (r < packed) {
-    _Float16* out = (_Float16*)A.out + (int64_t)(tile.row0 + t) * A.out_stride + (head * G + rr % G) * D;
+    int again = r;                               // r < packed here: its head is found again instead of kept
+    asm("" : "+v"(again));
+    _Float16* out =
+        (_Float16*)A.out + (int64_t)(tile.row0 + pos - tile.start) * A.out_stride + (head * G + again % G) * D;
     const float f = ref / Code<CODE>::kTop / l;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
