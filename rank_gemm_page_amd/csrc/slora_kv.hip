@@ -540,10 +540,12 @@ template <typename T> struct Frag;
 template <> struct Frag<_Float16> { typedef half8 type; };
 template <> struct Frag<float> { typedef float8v type; };
 
+// Operands of the products: fp16 takes the codes, which it holds exactly, fp32
+// the cached values, code * unit.
 template <int CODE>
-__device__ __forceinline__ void codes8(uint32_t a, uint32_t b, half8* r) { *r = Code<CODE>::halves(a, b); }
+__device__ __forceinline__ void codes8(uint32_t a, uint32_t b, float, half8* r) { *r = Code<CODE>::halves(a, b); }
 template <int CODE>
-__device__ __forceinline__ void codes8(uint32_t a, uint32_t b, float8v* r) { *r = floats8<CODE>(a, b); }
+__device__ __forceinline__ void codes8(uint32_t a, uint32_t b, float unit, float8v* r) { *r = floats8<CODE>(a, b) * unit; }
 
 __device__ __forceinline__ float4v mma(half8 a, half8 b, float4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -612,6 +614,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
   using F = typename Frag<T>::type;
   constexpr int NC = D / 64, NE = D / 32, NT = D / 16;
   constexpr int DC = D < 128 ? D : 128;          // columns joined at a time
+  // fp32 multiplies cached values and weights of at most 1, so that ranges may lie
+  // as far apart as fp32 numbers: sums in units of one block's range, which fp16
+  // codes need, would overflow or vanish beside another's.
+  constexpr bool values = sizeof(T) == 4;
   __shared__ float lds_o[4][kKvRows][DC + 4];
   __shared__ float lds_ml[4][kKvRows][2];
   __shared__ float lds_ref[4];
@@ -687,20 +693,22 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
     if (D < 256 && gi + 1 < ge) load(kn, vn, rkn, rvn);
     const int key0 = gi * kKvGroup;
 
+    // (a NaN range holds zero codes: its keys must be NaN, its values stay 0 for the rows that do not see them)
+    const float uk = values ? rk / Code<CODE>::kTop : 1.f, uv = values && rv > 0.f ? rv / Code<CODE>::kTop : 0.f;
     float4v s0 = {0.f, 0.f, 0.f, 0.f}, s1 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       F a;
-      codes8<CODE>(kf[c].x, kf[c].y, &a);
+      codes8<CODE>(kf[c].x, kf[c].y, uk, &a);
       s0 = mma(a, qf[2 * c], s0);
-      codes8<CODE>(kf[c].z, kf[c].w, &a);
+      codes8<CODE>(kf[c].z, kf[c].w, uk, &a);
       s0 = mma(a, qf[2 * c + 1], s0);
-      codes8<CODE>(kf[NC + c].x, kf[NC + c].y, &a);
+      codes8<CODE>(kf[NC + c].x, kf[NC + c].y, uk, &a);
       s1 = mma(a, qf[2 * c], s1);
-      codes8<CODE>(kf[NC + c].z, kf[NC + c].w, &a);
+      codes8<CODE>(kf[NC + c].z, kf[NC + c].w, uk, &a);
       s1 = mma(a, qf[2 * c + 1], s1);
     }
-    const float ck = rk / Code<CODE>::kTop * A.scale_log2;
+    const float ck = values ? A.scale_log2 : rk / Code<CODE>::kTop * A.scale_log2;
     float x[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) { x[j] = s0[j] * ck; x[4 + j] = s1[j] * ck; }
@@ -742,10 +750,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[n] *= f;
     }
-    // values of a block count in units of its range: the sums are kept in
+    // fp16: values of a block count in units of its range: the sums are kept in
     // units of a reference range, replaced when a block's is far from it
     float unit = 1.f;
-    if (rv > 0.f) {
+    if (!values && rv > 0.f) {
       unit = rv / ref;
       if (!(unit > 0x1p-10f && unit < 0x1p6f)) {
         const float f = ref / rv;
@@ -758,7 +766,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
     float p[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      p[j] = __builtin_amdgcn_exp2f(x[j] - m);
+      p[j] = __builtin_amdgcn_exp2f(x[j] - (values ? m + kLazy : m));
       l += p[j];
       p[j] *= unit;
     }
@@ -775,10 +783,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
       F a;
-      codes8<CODE>(vf[e].x, vf[e].y, &a);
+      codes8<CODE>(vf[e].x, vf[e].y, uv, &a);
       acc[2 * e] = mma(a, pf, acc[2 * e]);
       if (sizeof(T) == 2) acc[2 * e] = mma(a, pr, acc[2 * e]);
-      codes8<CODE>(vf[e].z, vf[e].w, &a);
+      codes8<CODE>(vf[e].z, vf[e].w, uv, &a);
       acc[2 * e + 1] = mma(a, pf, acc[2 * e + 1]);
       if (sizeof(T) == 2) acc[2 * e + 1] = mma(a, pr, acc[2 * e + 1]);
     }
@@ -796,7 +804,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
   if (g == 0) { lds_ml[wave][i][0] = m; lds_ml[wave][i][1] = l; }
-  if (lane == 0) lds_ref[wave] = ref / Code<CODE>::kTop;
+  if (lane == 0) lds_ref[wave] = values ? 1.f : ref / Code<CODE>::kTop;
   float* part = tile.splits > 1 ? A.part + ((int64_t)(tile.part + tile.split) * kv.n_kv + head) * kv_part_floats(D) : nullptr;
   constexpr int PER = DC / 16;                   // columns of a thread
   const int orow = tid >> 4, od = (tid & 15) * PER, gr = tile.tile * kKvRows + orow;

@@ -67,3 +67,64 @@ def test_weights_of_split_prompt_tiles_keep_their_bits(code):
         assert info["n_prompt_tiles"] > 1 and info["workspace_bytes"] > 0
         out = c.attend(st, q, ws, 0.125)
         weight_bits(c, out, q, [0], [20], starts, 0.125)
+
+
+def natural(c, out, q, seqs, counts, starts, scale, window=0):
+    """fp32: as KvCase.check_attend, with what numbers below 2^-126 may lose: weights are at most 1 and their sum is at
+    least 2^-8 (that of the largest score), so a value or a product that counts as 0 takes 2^-118 of the output, 2^-117
+    a key together."""
+    out, q = out.cpu().numpy().astype(np.float64), q.cpu().numpy()
+    at = 0
+    for s, n, start in zip(seqs, counts, starts):
+        want, weight, reach, _ = c.model.attend(s, 0, q[at:at + n], start, scale, window, start + n)
+        keys = start + n
+        bound = weight * (2 * (c.dim + 8) * 2.0 ** -24 * reach + 2.0 ** -20 + (keys + 8) * 2.0 ** -24) + keys * 2.0 ** -117
+        bound += half_step(np.abs(want) + bound, np.float32)
+        far = ~(np.abs(out[at:at + n] - want) <= bound)
+        assert not far.any(), (s, int(far.sum()), far.size, np.argwhere(far)[:4].tolist(), out[at:at + n][far][:4],
+                               want[far][:4])
+        at += n
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("gains", [(1.0, 1e-36, 1e-39, 1e30), (1e30, 1e-39, 1e-36, 1.0), (1e20, 1e-20, 0.0, 1e20),
+                                   (1e-39, 1.0, 1e-37, 0.0)])
+def test_fp32_value_ranges_far_apart(code, dim, gains):
+    """Values whose blocks differ by up to 1e69, four blocks a wave, in every order; with a window some rows see small
+    ones only."""
+    with KvCase(torch, "f32", code, 4, 2, dim, 32, max_tokens=544) as c:
+        for rows in (512, 5):
+            v = (c.draw(rows, 2).astype(np.float64) * np.tile(np.repeat(gains, 32), 4)[:rows, None, None]).astype(np.float32)
+            st, info, ws, q, starts = c.append([0], [rows], v=v)
+            for window in (0, 20, 150):
+                out = c.attend(st, q, ws, 0.125, window)
+                natural(c, out, q, [0], [rows], starts, 0.125, window)
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_fp32_value_ranges_far_apart_over_split_keys(code):
+    with KvCase(torch, "f32", code, 4, 2, 64, 32, max_seqs=1, max_tokens=2000) as c:
+        gains = np.tile(np.repeat([1.0, 1e-39, 1e25, 1e-36, 1e10], 32), 11)[:1700, None, None]
+        v = (c.draw(1700, 2).astype(np.float64) * gains).astype(np.float32)
+        c.append([0], [1700], v=v)
+        st, info, ws, q, starts = c.append([0], [2])
+        assert info["workspace_bytes"] > 0
+        for window in (0, 60, 500):
+            out = c.attend(st, q, ws, 0.125, window)
+            natural(c, out, q, [0], [2], starts, 0.125, window)
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_fp32_magnitudes_that_products_of_codes_would_pass(code):
+    """Large q on small keys, and values near the largest: scores of about 1 and outputs that fp32 holds, though
+    q times a code, or a sum of codes in units of the range, would pass it."""
+    with KvCase(torch, "f32", code, 2, 2, 64, 32, rot=0) as c:
+        for rows in (100, 3):
+            k = (c.draw(rows, 2).astype(np.float64) * 1e-37).astype(np.float32)
+            v = (c.rng.uniform(-1, 1, (rows, 2, 64)) * 1e36).astype(np.float32)
+            x = (c.draw(rows, 2).astype(np.float64) * 1e36).astype(np.float32)
+            st, info, ws, q, starts = c.append([0], [rows], k=k, v=v, q=x)
+            for scale in (1.0, -2.0):
+                out = c.attend(st, q, ws, scale)
+                natural(c, out, q, [0], [rows], starts, scale)
