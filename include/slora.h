@@ -518,9 +518,16 @@ const char* slora_last_error(void);
  *
  * Ordering: uploads and launches of one cache go to one stream, or the caller
  * orders them (a launch reads the page table that earlier uploads wrote, and
- * attention reads what earlier appends stored).  Launches may be captured into
- * a HIP graph; uploads may not.  A replayed append stores the same positions
- * again from what its input buffers then hold; ranges only grow. */
+ * attention reads what earlier appends stored).  Tokens enter a block in their
+ * order, because its ranges stand for all of them: a layer's append takes up
+ * where the layer's last one ended, or stores the same positions again from what
+ * its input buffers then hold, as long as they are the last ones stored in the
+ * step's blocks.  (Blocks that the step begins then take their ranges anew; the
+ * ranges of others only grow.)  Any other order is refused.  Launches may be
+ * captured into a HIP graph; uploads may not.  A captured append counts as
+ * launched when it is captured; its replays are not seen, and keep to the same
+ * rule: not after a later step's append to the same blocks, nor after a sequence
+ * of the step was dropped. */
 typedef struct slora_kv slora_kv;
 typedef struct slora_kv_step slora_kv_step;
 
@@ -604,7 +611,8 @@ slora_status slora_kv_step_upload(slora_kv_step* step, void* dev_meta, size_t de
  * parts of one projection's output); pointers are 16-byte aligned and strides
  * are multiples of 16 bytes and at least heads * head_dim.  q_out may be q
  * itself (same pointer and stride), else they do not overlap; q and q_out may
- * both be NULL.  cos_sin holds every position of the step (n_positions >
+ * both be NULL.  SLORA_E_INVAL where the order of appends is not kept (see
+ * "Ordering").  cos_sin holds every position of the step (n_positions >
  * the largest one); without rotation (rot_dim 0) it may be NULL.  One launch on
  * `stream`.  A reread step is refused. */
 slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* step, int32_t layer, const void* q,

@@ -30,6 +30,7 @@ struct Seq {
   int32_t entered = 0;     // of these, in the device's page table
   uint64_t gen = 0;        // counts drops
   std::vector<int32_t> pages;   // [block][layer][head]
+  std::vector<int32_t> stored;  // [block][layer] tokens that appends have been launched for
 };
 
 // Checks a description against a pool; the block size and blocks of the
@@ -235,6 +236,19 @@ slora_status check_rows(const std::string& f, const char* name, const slora_kv* 
   return SLORA_OK;
 }
 
+// A range stands for its whole block, so tokens enter a block in their order: an
+// append takes up where the last one of the layer ended, or repeats it.
+slora_status check_order(const std::string& f, const slora_kv* kv, const slora_kv_step* st, int32_t layer) {
+  for (const KvBlock& b : st->blocks) {
+    const int32_t have = kv->seqs[b.seq].stored[(size_t)b.block * kv->d.n_layers + layer];
+    if (have < b.slot0)
+      return fail(SLORA_E_INVAL, f + ": earlier tokens of a block have not been appended in this layer");
+    if (have > b.slot1)
+      return fail(SLORA_E_INVAL, f + ": later tokens of a block have been appended in this layer");
+  }
+  return SLORA_OK;
+}
+
 slora_status launched(const std::string& f, hipError_t e) {
   if (e == hipSuccess) return SLORA_OK;
   return fail(SLORA_E_HIP, f + " launch: " + hipGetErrorString(e));
@@ -293,6 +307,7 @@ slora_status slora_kv_drop(slora_kv* kv, int32_t seq) {
   }
   s.pages.clear();
   s.pages.shrink_to_fit();
+  s.stored.clear();
   s.len = 0;
   s.blocks = s.entered = 0;
   ++s.gen;
@@ -390,6 +405,8 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
       std::vector<int32_t>& pages = kv->seqs[seqs[i]].pages;
       const size_t want = (size_t)(st->ends[i] * kv->per_block());
       if (want > pages.capacity()) pages.reserve(std::max(want, 2 * pages.capacity()));
+      std::vector<int32_t>& stored = kv->seqs[seqs[i]].stored;
+      stored.resize(std::max(stored.size(), (size_t)st->ends[i] * kv->d.n_layers), 0);
     }
     slora_status got = slora_alloc_pages(kv->pool, kv->d.cls, need, ids.data());
     if (got != SLORA_OK) {
@@ -499,6 +516,7 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* st, int32_t laye
       return fail(SLORA_E_INVAL, f + ": cos_sin must be non-NULL and 16-byte aligned");
     if (n_positions < st->max_len) return fail(SLORA_E_INVAL, f + ": cos_sin does not hold every position of the step");
   }
+  if ((ok = check_order(f, kv, st, layer)) != SLORA_OK) return ok;
   if (!st->dev) return fail(SLORA_E_INVAL, f + ": step not uploaded (call slora_kv_step_upload)");
   if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
   KvAppend A{};
@@ -521,7 +539,10 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* st, int32_t laye
   A.v_stride = v_stride;
   A.cos_sin = cos_sin;
   A.row_pos = reinterpret_cast<const int32_t*>(st->dev + st->row_pos_off());
-  return launched(f, launch_kv_append(A, static_cast<hipStream_t>(stream)));
+  ok = launched(f, launch_kv_append(A, static_cast<hipStream_t>(stream)));
+  if (ok == SLORA_OK)
+    for (const KvBlock& b : st->blocks) kv->seqs[b.seq].stored[(size_t)b.block * kv->d.n_layers + layer] = b.slot1;
+  return ok;
 }
 
 slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* st, int32_t layer, const void* q, int64_t q_stride,

@@ -128,3 +128,64 @@ def test_fp32_magnitudes_that_products_of_codes_would_pass(code):
             for scale in (1.0, -2.0):
                 out = c.attend(st, q, ws, scale)
                 natural(c, out, q, [0], [rows], starts, scale)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("first,then", [(10, 5), (1, 1), (40, 1), (3, 40), (33, 2)])
+def test_a_step_is_appended_again_only_while_its_blocks_end_with_it(code, first, then):
+    """An older step's append would leave the tokens behind it in its last block at another range: refused, and the
+    cache stays as it was."""
+    with KvCase(torch, "f16", code, 4, 2, 64, 32) as c:
+        stream = torch.cuda.current_stream()
+        x = [[c.draw(n, 2, g) for _ in range(2)] for n, g in ((first, 0.1), (then, 8.0))]
+        old, *_ = c.append([0], [first], k=x[0][0], v=x[0][1])
+        S.slora_kv_append(c.kv, old, 0, c.device(x[0][0]), c.device(x[0][1]), cos_sin=c.cos_sin, stream=stream)
+        new, *_ = c.append([0], [then], k=x[1][0], v=x[1][1])
+        for step, (k, v) in ((new, x[1]), (old, x[0])):
+            if step is old:
+                with pytest.raises(S.SloraError) as e:
+                    S.slora_kv_append(c.kv, step, 0, c.device(k), c.device(v), cos_sin=c.cos_sin, stream=stream)
+                assert e.value.status == S.SLORA_E_INVAL
+            else:
+                S.slora_kv_append(c.kv, step, 0, c.device(k), c.device(v), cos_sin=c.cos_sin, stream=stream)
+            c.check_read([0])
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_a_step_that_ends_its_block_is_appended_again_at_any_time(code):
+    with KvCase(torch, "f16", code, 4, 2, 64, 32) as c:
+        k, v = c.draw(64, 2), c.draw(64, 2)
+        old, *_ = c.append([0], [64], k=k, v=v)
+        c.append([0], [7], 3.0)
+        S.slora_kv_append(c.kv, old, 0, c.device(k), c.device(v), cos_sin=c.cos_sin, stream=torch.cuda.current_stream())
+        c.check_read([0])
+        c.append([0], [7], 5.0)
+        c.check_read([0])
+
+
+def test_steps_built_ahead_are_appended_in_order():
+    """Two steps of one block built and uploaded before either runs: the second is refused until the first is stored,
+    layer by layer; a dropped sequence begins anew."""
+    with KvCase(torch, "f16", 0, 4, 2, 64, 32, n_layers=2) as c:
+        stream = torch.cuda.current_stream()
+        steps = [c.step([1], [n])[0] for n in (6, 4, 30)]
+        x = [[c.device(c.draw(n, 2)) for _ in range(2)] for n in (6, 4, 30)]
+
+        def put(i, layer):
+            S.slora_kv_append(c.kv, steps[i], layer, *x[i], cos_sin=c.cos_sin, stream=stream)
+
+        for layer in range(2):
+            for i in range(3):
+                for late in range(i + 1, 3):
+                    with pytest.raises(S.SloraError) as e:
+                        put(late, layer)
+                    assert e.value.status == S.SLORA_E_INVAL
+                put(i, layer)
+                c.model.append(1, layer, *(t.cpu().numpy() for t in x[i]))
+            c.check_read([1], layer)
+        S.slora_kv_drop(c.kv, 1)
+        for layer in range(2):
+            for w in range(2):
+                del c.model.codes[1, layer, w], c.model.range[1, layer, w]
+        c.append([1], [9])
+        c.check_read([1])
