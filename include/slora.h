@@ -492,7 +492,8 @@ const char* slora_last_error(void);
  *     code * range / 448   (SLORA_KV_FP8: code = an e4m3 number)
  *
  * and is the nearest one to the appended value (ties to even), computed in 64
- * bits as value * (127 or 448 / range).  When a later append raises the range
+ * bits as value * (127 or 448 / range); a range is rounded to fp32, and where it
+ * is subnormal a value that passes it takes the last code.  When a later append raises the range
  * of a block that is partly filled, its older codes are coded again:
  * nearest(code * (old range / new range)).  A value that is not finite (or,
  * after the rotation, beyond fp32) makes the range NaN, and every key (or
@@ -626,7 +627,8 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* step, int32_t la
  *     s_j = scale * q[t, h] . k_j      out[t, h] = sum_j softmax(s)_j v_j
  *
  * over positions j <= p, with window > 0 also j > p - window (0: no window).
- * k and v are the cached values; products are accumulated in fp32, the softmax
+ * k and v are the cached values; products are accumulated in fp32 (numbers below
+ * 2^-126 may count as 0 there), the softmax
  * is held in fp32, and out is rounded once to the pool dtype.  q is [n_rows]
  * rotated rows (slora_kv_append's q_out), q and out laid out as for
  * slora_kv_append.  workspace is device memory of at least workspace_bytes,

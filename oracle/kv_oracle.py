@@ -21,7 +21,8 @@ def e4m3(x):
 
 
 def nearest(code, x):
-    return np.rint(x) if code == INT8 else e4m3(np.asarray(x, np.float64).astype(np.float32))
+    """Nearest code; only a value above its subnormal (rounded) range meets the ends."""
+    return np.clip(np.rint(x), -127.0, 127.0) if code == INT8 else e4m3(np.asarray(x, np.float64).astype(np.float32))
 
 
 def angles(n_positions, rot, base=10000.0):

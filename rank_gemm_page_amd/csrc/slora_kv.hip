@@ -48,10 +48,12 @@ template <> struct Code<SLORA_KV_INT8> {
   }
   static __device__ __forceinline__ float value(uint32_t byte) { return (float)(int)byte - 128.f; }
   // Added to 1.5 * 2^52, a number this small is rounded to an integer (ties to
-  // even) that stands in the low bits.
+  // even) that stands in the low bits.  A subnormal range may lie below its
+  // largest value by half a unit, which takes codes up to half as much again:
+  // they are held at the largest one.
   static __device__ __forceinline__ uint32_t nearest(double x) {
 #pragma clang fp contract(off)
-    return (uint32_t)__double2loint(x + (0x1.8p52 + 128.)) & 0xFF;
+    return (uint32_t)min(max(__double2loint(x + (0x1.8p52 + 128.)), 1), 255);
   }
 };
 
@@ -70,7 +72,8 @@ template <> struct Code<SLORA_KV_FP8> {
   }
   // The definition rounds the 64-bit product to fp32 and then to e4m3.
   static __device__ __forceinline__ uint32_t nearest(double x) {
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32((float)x, 0.f, 0, false) & 0xFF;
+    const float y = __builtin_amdgcn_fmed3f((float)x, -kTop, kTop);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, 0.f, 0, false) & 0xFF;
   }
 };
 
@@ -1189,8 +1192,13 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
 // rows are stored in two halves of every 32 bytes, which such stores do not
 // merge (3.2 TB/s against 4.6).
 
+// Fp32 values are multiplied in 64 bits, where the unit of a small range is as
+// exact as any: in fp32, ranges below 127 times the smallest number read as 0.
+template <typename T> struct Unit { typedef float type; };
+template <> struct Unit<float> { typedef double type; };
+
 template <typename T, int CODE>
-__device__ __forceinline__ void put8(T* p, uint32_t a, uint32_t b, float unit) {
+__device__ __forceinline__ void put8(T* p, uint32_t a, uint32_t b, typename Unit<T>::type unit) {
   typename Vec<T>::v8 y;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -1237,7 +1245,8 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvRead R) {
         vw[n] = ld16(vbase + ((int64_t)(group0 + (u >> (ush + 5))) << (ush + 9)) +
                      ((u >> 6) & ((1 << (ush - 1)) - 1)) * 1024 + lane * 16);
     }
-    const float uk = range[0] / C::kTop, uv = range[1] / C::kTop;
+    typedef typename Unit<T>::type U;
+    const U uk = (U)range[0] / C::kTop, uv = (U)range[1] / C::kTop;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const int u = u0 + tid + n * kThreads;

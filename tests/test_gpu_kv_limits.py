@@ -189,3 +189,24 @@ def test_steps_built_ahead_are_appended_in_order():
                 del c.model.codes[1, layer, w], c.model.range[1, layer, w]
         c.append([1], [9])
         c.check_read([1])
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("size", [2e-45, 1e-44, 1e-42, 1e-39])
+def test_fp32_subnormal_ranges(code, size):
+    """Ranges of a few units of the smallest number: codes stay in -127 .. 127 and values within their steps.  Rotated
+    keys lie between the units, so that the range is rounded from them; single tokens, pieces and older codes coded
+    again."""
+    with KvCase(torch, "f32", code, 4, 2, 64, 32, max_tokens=128) as c:
+        unit = 2.0 ** -149
+        for n, gain in ((1, 1.0), (1, 2.0), (29, 1.5), (1, 3.0), (40, 1.0)):
+            k, v = ((np.rint(c.rng.uniform(-1, 1, (n, 2, 64)) * gain * size / unit) * unit).astype(np.float32)
+                    for _ in range(2))
+            c.append([0], [n], k=k, v=v)
+        st, _, _ = c.step([0], [c.model.length(0)], True)
+        got = [torch.zeros((c.model.length(0), 2, 64), dtype=torch.float32, device="cuda:0") for _ in range(2)]
+        S.slora_kv_read(c.kv, st, 0, got[0], got[1], torch.cuda.current_stream())
+        for what in range(2):
+            want, have = c.model.values(0, 0, what), got[what].cpu().numpy().astype(np.float64)
+            # the value is rounded once; half a unit
+            assert (np.abs(have - want) <= 2.0 ** -24 * np.abs(want) + unit / 2).all()
