@@ -83,9 +83,17 @@ class KvStepInfo(ctypes.Structure):
                  "reserved0")] + [("meta_bytes", c_size_t), ("workspace_bytes", c_size_t)]
 
 
+class Pool(c_void_p):
+    """Handle of a pool; ``dtype`` names its elements' type, ``device`` is the index of its pages' GPU where they were
+    given as tensors (None where as addresses)."""
+    dtype = device = None
+
+
 class KvCache(c_void_p):
     """Handle of a cache; ``desc`` holds its description, ``heads`` its query and kv heads, ``rot`` its rotated
-    elements."""
+    elements, ``dtype`` and ``device`` the pool's; ``element`` and ``single`` are the tensors' own names of
+    that type and of fp32, once met, ``api`` the library."""
+    element = single = None
 
 
 class KvStep(c_void_p):
@@ -218,8 +226,11 @@ def slora_pool_create(dtype: int, h_in: int, h_out: int, n_proj: int, max_adapte
                 raise ValueError("free_order[c] must have n_pages[c] entries")
             keep.append(fo)
             d.free_order[c] = _i32p(fo)
-    out = c_void_p()
+    out = Pool()
     _check(lib().slora_pool_create(ctypes.byref(d), ctypes.byref(out)), "slora_pool_create")
+    out.dtype = "float16" if dtype == SLORA_F16 else "float32"
+    if hasattr(class_base[0], "get_device"):
+        out.device = class_base[0].get_device()
     return out
 
 
@@ -502,10 +513,34 @@ def slora_kv_device_bytes(pool, **desc) -> int:
     return n
 
 
+def _type_name(dtype) -> str:
+    return str(dtype).rpartition(".")[2]
+
+
+def _on_device(x, device, what: str) -> None:
+    """Refuses a tensor in host memory or, where the pages' GPU is known, on another one."""
+    at = x.get_device()
+    if at < 0 or (device is not None and at != device):
+        raise ValueError(f"{what} must be on the pool's GPU, not on {x.device}")
+
+
+def _area(x, nbytes: int, device, what: str) -> int:
+    """Address of device memory of nbytes: a contiguous tensor that holds them, or a raw address."""
+    if not hasattr(x, "get_device"):
+        return _ptr(x)
+    if x.nbytes < nbytes or not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and hold {nbytes} bytes, has {x.nbytes}")
+    if x.get_device() != device:
+        _on_device(x, device, what)
+    return x.data_ptr()
+
+
 def slora_kv_create(pool, dev, dev_bytes: int, **desc) -> KvCache:
     kv = KvCache()
-    kv.desc = KvDesc(**desc)
-    _check(lib().slora_kv_create(pool, ctypes.byref(kv.desc), _ptr(dev), int(dev_bytes), ctypes.byref(kv)),
+    kv.api, kv.desc = lib(), KvDesc(**desc)
+    kv.dtype, kv.device = getattr(pool, "dtype", None), getattr(pool, "device", None)
+    dev = _area(dev, dev_bytes, kv.device, "dev")
+    _check(lib().slora_kv_create(pool, ctypes.byref(kv.desc), dev, int(dev_bytes), ctypes.byref(kv)),
            "slora_kv_create")
     kv.heads, kv.rot = (kv.desc.n_heads, kv.desc.n_kv_heads), kv.desc.rot_dim
     return kv
@@ -555,13 +590,15 @@ def slora_kv_step_get_info(step) -> dict:
 
 
 def slora_kv_step_upload(step, dev_meta, dev_meta_bytes: int, stream=None) -> None:
-    _check(lib().slora_kv_step_upload(step, _ptr(dev_meta), int(dev_meta_bytes), _stream(stream)),
+    dev_meta = _area(dev_meta, dev_meta_bytes, step.kv.device, "dev_meta")
+    _check(lib().slora_kv_step_upload(step, dev_meta, int(dev_meta_bytes), _stream(stream)),
            "slora_kv_step_upload")
 
 
 def _rows(x, step, heads: int, stride):
     """(address, stride in elements between tokens) of a [n_rows, heads, head_dim] operand: a tensor of that shape
-    whose heads are contiguous, or a raw address with its stride (contiguous by default)."""
+    and the pool's type on its GPU, whose heads are contiguous, or a raw address with its stride (contiguous by
+    default)."""
     if x is None:
         return 0, 0
     dim = step.dim
@@ -574,25 +611,54 @@ def _rows(x, step, heads: int, stride):
         raise ValueError(f"expected at least {step.n_rows} rows of {heads} heads of {dim}, got {tuple(x.shape)}")
     if n and (sd != 1 or (sh != dim and heads > 1)):
         raise ValueError("the heads of a row must be contiguous")
+    kv = step.kv
+    if x.dtype is not kv.element:
+        if kv.dtype is not None and _type_name(x.dtype) != kv.dtype:
+            raise ValueError(f"expected the pool's type, {kv.dtype}, got {x.dtype}")
+        kv.element = x.dtype
+    if x.get_device() != kv.device:
+        _on_device(x, kv.device, "rows")
     if stride is None:
         stride = sn if n > 1 else heads * dim
+    elif step.n_rows:
+        end = x.storage_offset() + (step.n_rows - 1) * int(stride) + heads * dim
+        if end * x.element_size() > x.untyped_storage().nbytes():
+            raise ValueError(f"{step.n_rows} rows {stride} elements apart do not fit the tensor's memory")
     return x.data_ptr(), stride
+
+
+def _angles(x, n_positions, kv):
+    """(address, positions) of a table of cosines and sines."""
+    if not hasattr(x, "get_device"):
+        return _ptr(x), n_positions or 0
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != kv.rot or not x.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous [n_positions, rot_dim] tensor")
+    if x.dtype is not kv.single:
+        if _type_name(x.dtype) != "float32":
+            raise ValueError(f"cos_sin must be fp32, got {x.dtype}")
+        kv.single = x.dtype
+    if x.get_device() != kv.device:
+        _on_device(x, kv.device, "cos_sin")
+    if n_positions is None:
+        n_positions = shape[0]
+    elif n_positions > shape[0]:
+        raise ValueError(f"cos_sin holds {shape[0]} positions, not {n_positions}")
+    return x.data_ptr(), n_positions
 
 
 def slora_kv_append(kv, step, layer: int, k, v, q=None, q_out=None, cos_sin=None, stream=None, k_stride=None,
                     v_stride=None, q_stride=None, q_out_stride=None, n_positions=None) -> None:
     """cos_sin: a contiguous fp32 tensor [n_positions, rot_dim], or a raw address with n_positions."""
     heads, kv_heads = kv.heads
-    if cos_sin is not None and n_positions is None:
-        if cos_sin.dim() != 2 or cos_sin.shape[1] != kv.rot or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous [n_positions, rot_dim] tensor")
-        n_positions = cos_sin.shape[0]
+    cs, n_positions = _angles(cos_sin, n_positions, kv)
     qp, qs = _rows(q, step, heads, q_stride)
     op, os_ = _rows(q_out, step, heads, q_out_stride)
     kp, ks = _rows(k, step, kv_heads, k_stride)
     vp, vs = _rows(v, step, kv_heads, v_stride)
-    _check(lib().slora_kv_append(kv, step, layer, qp, qs, op, os_, kp, ks, vp, vs, _ptr(cos_sin), n_positions or 0,
-                                 _stream(stream)), "slora_kv_append")
+    status = kv.api.slora_kv_append(kv, step, layer, qp, qs, op, os_, kp, ks, vp, vs, cs, n_positions, _stream(stream))
+    if status:
+        _check(status, "slora_kv_append")
 
 
 def slora_kv_attend(kv, step, layer: int, q, out, scale: float, window: int = 0, workspace=None,
@@ -600,12 +666,17 @@ def slora_kv_attend(kv, step, layer: int, q, out, scale: float, window: int = 0,
     heads = kv.heads[0]
     qp, qs = _rows(q, step, heads, q_stride)
     op, os_ = _rows(out, step, heads, out_stride)
-    _check(lib().slora_kv_attend(kv, step, layer, qp, qs, op, os_, scale, window, _ptr(workspace),
-                                 int(workspace_bytes), _stream(stream)), "slora_kv_attend")
+    workspace = _area(workspace, workspace_bytes, kv.device, "workspace")
+    status = kv.api.slora_kv_attend(kv, step, layer, qp, qs, op, os_, scale, window, workspace, int(workspace_bytes),
+                                    _stream(stream))
+    if status:
+        _check(status, "slora_kv_attend")
 
 
 def slora_kv_read(kv, step, layer: int, k=None, v=None, stream=None, k_stride=None, v_stride=None) -> None:
     kv_heads = kv.heads[1]
     kp, ks = _rows(k, step, kv_heads, k_stride)
     vp, vs = _rows(v, step, kv_heads, v_stride)
-    _check(lib().slora_kv_read(kv, step, layer, kp, ks, vp, vs, _stream(stream)), "slora_kv_read")
+    status = kv.api.slora_kv_read(kv, step, layer, kp, ks, vp, vs, _stream(stream))
+    if status:
+        _check(status, "slora_kv_read")

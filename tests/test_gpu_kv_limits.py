@@ -35,8 +35,8 @@ def weight_bits(c, out, q, seqs, counts, starts, scale, window=0):
             want, weight, reach, spread = c.model.attend(s, 0, q[at:at + n], start, scale, window, start + n)
             r = c.model.range[s, 0, 1]
             ratio = min(1024.0, r.max() / r[r > 0].min())
-            bound = weight * (2 * (c.dim + 8) * 2.0 ** -24 * reach + 2.0 ** -20 + (start + n + 8) * 2.0 ** -24 + 2.0 ** -22)
-            bound += spread * 2.0 ** -25 * ratio
+            bound = weight * (2 * (c.dim + 8) * 2.0 ** -24 * reach + 2.0 ** -20 + (start + n + 8) * 2.0 ** -24)
+            bound += weight * 2.0 ** -22 + spread * 2.0 ** -25 * ratio
             bound += half_step(np.abs(want) + bound, c.np_dtype)
             far = np.abs(out[at:at + n] - want) > bound
             assert not far.any(), (s, int(far.sum()), far.size, np.argwhere(far)[:4].tolist())
@@ -47,7 +47,7 @@ def weight_bits(c, out, q, seqs, counts, starts, scale, window=0):
 @pytest.mark.parametrize("dim,heads,kv", [(64, 4, 4), (128, 8, 2), (256, 2, 1)])
 @pytest.mark.parametrize("rows,window", [(10, 0), (150, 0), (150, 5)])
 def test_weights_of_prompt_tiles_keep_their_bits(code, dim, heads, kv, rows, window):
-    """10 rows of up to 4 query heads a kv head take the row tiles, 150 the prompt tiles: the same bound for both.  Small
+    """10 rows of up to 4 query heads a kv head take the row tiles, 150 the prompt tiles: one bound for both.  Small
     scores keep the bound of their fp32 sums below a weight's 11th bit, and few keys its rounding from averaging out."""
     scale = 0.25 / np.sqrt(dim)
     with KvCase(torch, "f16", code, heads, kv, dim, 32, max_tokens=600) as c:
@@ -78,7 +78,8 @@ def natural(c, out, q, seqs, counts, starts, scale, window=0):
     for s, n, start in zip(seqs, counts, starts):
         want, weight, reach, _ = c.model.attend(s, 0, q[at:at + n], start, scale, window, start + n)
         keys = start + n
-        bound = weight * (2 * (c.dim + 8) * 2.0 ** -24 * reach + 2.0 ** -20 + (keys + 8) * 2.0 ** -24) + keys * 2.0 ** -117
+        bound = weight * (2 * (c.dim + 8) * 2.0 ** -24 * reach + 2.0 ** -20 + (keys + 8) * 2.0 ** -24)
+        bound += keys * 2.0 ** -117
         bound += half_step(np.abs(want) + bound, np.float32)
         far = ~(np.abs(out[at:at + n] - want) <= bound)
         assert not far.any(), (s, int(far.sum()), far.size, np.argwhere(far)[:4].tolist(), out[at:at + n][far][:4],
@@ -95,7 +96,8 @@ def test_fp32_value_ranges_far_apart(code, dim, gains):
     ones only."""
     with KvCase(torch, "f32", code, 4, 2, dim, 32, max_tokens=544) as c:
         for rows in (512, 5):
-            v = (c.draw(rows, 2).astype(np.float64) * np.tile(np.repeat(gains, 32), 4)[:rows, None, None]).astype(np.float32)
+            gain = np.tile(np.repeat(gains, 32), 4)[:rows, None, None]
+            v = (c.draw(rows, 2).astype(np.float64) * gain).astype(np.float32)
             st, info, ws, q, starts = c.append([0], [rows], v=v)
             for window in (0, 20, 150):
                 out = c.attend(st, q, ws, 0.125, window)
