@@ -1338,12 +1338,17 @@ hipError_t launch_kv_append(const KvAppend& A0, hipStream_t stream) {
 
 hipError_t launch_kv_attend(const KvAttend& A, hipStream_t stream) {
   const bool half = A.kv.dtype == SLORA_F16;
-  // Three workgroups a CU (32 keys staged at a time) hide each other's staging
-  // better than two with 64: prompts of 512 tokens 149 against 157 us, of 4096
-  // 668 against 700 us.  But four of about the same length on every CU leave the
-  // last one alone on it (612 against 560 us): those run two and two.
+  // Heads of 128 run two workgroups a CU that stage 64 keys at a time, or three
+  // that stage 32.  What counts is how often the places of the chip fill: three
+  // where that saves a round, two, which are faster each, where it does not.
+  // us with two | three, 32 query and kv heads, prompts of 512 tokens, n of them
+  // (n / 2 workgroups a CU): 4: 27.7 | 30.9, 6: 39.5 | 33.9, 8: 46.0 | 45.2, 10:
+  // 55 | 53, 14: 74 | 67, 16: 79 | 74, 32: 163 | 157; 32 prompts of 64 to 512
+  // (11.1 a CU): 86 | 77; with 64 query and 8 kv heads 2048 tokens after 6001 (4 a
+  // CU): 684 | 719, 512 after 16000 (4 a CU): 433 | 451; against the rule, with 32
+  // and 8 heads one prompt of 4096 (5 a CU): 239 | 247.
   const int64_t prompts = (int64_t)A.n_prompts * A.kv.n_kv;
-  const bool triple = (prompts + kKvCus - 1) / kKvCus != 4;
+  const bool triple = (prompts - 1) / (3 * kKvCus) < (prompts - 1) / (2 * kKvCus);
   hipError_t e = run(A.kv.code == SLORA_KV_INT8 ? prompt_of<SLORA_KV_INT8>(A.kv.dim, triple)
                                                 : prompt_of<SLORA_KV_FP8>(A.kv.dim, triple),
                      prompts, A, stream);

@@ -1,9 +1,12 @@
-"""The 8-bit paged KV cache on the GPU at the limits of its types and of its order of calls."""
+"""The 8-bit paged KV cache on the GPU at the limits of its types, of its order of calls and of its launches."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
+from oracle import kv_oracle as O  # noqa: E402
 from rank_gemm_page_amd import slora as S  # noqa: E402
 from tests.kv_case import KvCase, half_step  # noqa: E402
 
@@ -212,3 +215,53 @@ def test_fp32_subnormal_ranges(code, size):
             want, have = c.model.values(0, 0, what), got[what].cpu().numpy().astype(np.float64)
             # the value is rounded once; half a unit
             assert (np.abs(have - want) <= 2.0 ** -24 * np.abs(want) + unit / 2).all()
+
+
+def some_heads(c, kv_heads):
+    """The model's part for a few kv heads, and their query heads."""
+    g = c.n_heads // c.n_kv
+    m = O.KvModel(c.desc["code"], g * len(kv_heads), len(kv_heads), c.dim, c.desc["block_tokens"])
+    m.codes = {key: x[:, kv_heads] for key, x in c.model.codes.items()}
+    m.range = {key: x[:, kv_heads] for key, x in c.model.range.items()}
+    return SimpleNamespace(model=m, dim=c.dim, np_dtype=c.np_dtype), [h * g + i for h in kv_heads for i in range(g)]
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("seqs,rows,window", [(1, 300, 0), (3, 300, 0), (3, 300, 90), (5, 280, 0), (6, 300, 0)])
+def test_prompts_that_fill_the_chip_once_and_more(code, seqs, rows, window):
+    """192 to 1152 workgroups of 64 heads of 128: both forms of the prompt kernel, one round of its places and several."""
+    with KvCase(torch, "f16", code, 64, 64, 128, 32, max_seqs=6, max_tokens=400) as c:
+        ids = list(range(seqs))
+        c.append(ids, [17 * i for i in ids])
+        st, info, ws, q, starts = c.append(ids, [rows] * seqs)
+        assert info["n_prompt_tiles"] == 3 * seqs
+        out = c.attend(st, q, ws, 0.09, window)
+        part, heads = some_heads(c, [0, 37, 63])
+        weight_bits(part, out[:, heads], q[:, heads], ids, [rows] * seqs, starts, 0.09, window)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dim,heads,kv,block", [(128, 8, 2, 64), (256, 8, 2, 32), (128, 64, 1, 32)])
+@pytest.mark.parametrize("window", [0, 700, 10])
+def test_split_prompt_tiles_of_wide_heads(code, dim, heads, kv, block, window):
+    """Keys split over workgroups and joined, also where a window leaves some of them nothing; and a single token whose
+    64 query heads share a kv head."""
+    with KvCase(torch, "f16", code, heads, kv, dim, block, max_seqs=2, max_tokens=2500) as c:
+        rows = [1, 1] if heads == 64 else [20, 13]
+        c.append([0, 1], [2400, 1500])
+        st, info, ws, q, starts = c.append([0, 1], rows)
+        assert info["n_prompt_tiles"] > 2 and info["n_row_tiles"] == 0 and info["workspace_bytes"] > 0
+        out = c.attend(st, q, ws, 1 / np.sqrt(dim), window)
+        weight_bits(c, out, q, [0, 1], rows, starts, 1 / np.sqrt(dim), window)
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_few_rows_after_a_long_context_fill_the_chip_with_splits(code):
+    """64 rows of 4 query heads a kv head after 30000 tokens: near a thousand workgroups, 62 splits a tile."""
+    with KvCase(torch, "f16", code, 32, 8, 128, 32, max_seqs=1, max_tokens=30100) as c:
+        c.append([0], [30000])
+        st, info, ws, q, starts = c.append([0], [64])
+        assert 768 < info["n_prompt_tiles"] * 8 <= 1024
+        out = c.attend(st, q, ws, 0.09)
+        part, heads = some_heads(c, [5])
+        weight_bits(part, out[:, heads], q[:, heads], [0], [64], starts, 0.09)
