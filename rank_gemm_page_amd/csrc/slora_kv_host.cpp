@@ -139,12 +139,18 @@ namespace {
 constexpr int64_t kMinGroups = 8, kWantGroups = 1536;
 
 // Sequences with at least kPromptMin packed rows (query heads of a kv head times
-// rows) take the prompt tiles (fp16).  Around there: 50 rows after 2000 tokens
-// 134 us in them against 152 in row tiles, 56 rows after 1000 tokens 49 in both,
-// 40 after 1000 tokens 47 against 39.  Their keys are split only where a launch
-// has fewer tiles than kWantPrompts, the chip's places over: a workgroup takes
-// at least kPromptGroups groups.
-constexpr int64_t kPromptMin = 48, kPromptGroups = 16, kWantPrompts = 1024;
+// rows), or kFreshMin where nothing was cached before them, take the prompt tiles
+// (fp16), which do the work of 128 rows however few there are.  Row | prompt
+// tiles, us, heads of 128: 16 sequences of 1000 tokens, 32 heads, 48 more rows 53
+// | 102, 64: 69 | 99, 96: 93 | 104, 128: 119 | 115, 160: 146 | 123; of 2000 tokens
+// 64: 125 | 146, 96: 173 | 162; with 32 heads on 8 16 rows 40 | 46, 28: 53 | 51;
+// 32 fresh prompts of 48 rows 18 | 16, 64: 23 | 17, 96: 33 | 24.  The rule leaves
+// out how many sequences there are: one with 24 rows after 1000 tokens takes 9 |
+// 25, after 20000 tokens 59 | 42; a single token of 96 query heads a kv head 9 | 22
+// after 800 tokens, 74 | 32 after 20000, for 32 such requests of 2000 54 | 56.
+// Their keys are split only where a launch has fewer tiles than kWantPrompts, two
+// rounds of two workgroups a CU: a workgroup takes at least kPromptGroups groups.
+constexpr int64_t kPromptMin = 96, kFreshMin = 48, kPromptGroups = 16, kWantPrompts = 1024;
 
 // Tiles of 128 packed rows for long runs of rows (fp16), and row tiles of 16 for
 // the others, with their key splits, longest first.
@@ -152,7 +158,7 @@ void build_tiles(slora_kv_step* st) {
   const slora_kv_desc& d = st->kv->d;
   const int32_t G = d.n_heads / d.n_kv_heads;
   const bool half = st->kv->info.dtype == SLORA_F16;
-  auto prompt = [&](const StepSeq& s) { return half && (int64_t)s.rows * G >= kPromptMin; };
+  auto prompt = [&](const StepSeq& s) { return half && (int64_t)s.rows * G >= (s.start ? kPromptMin : kFreshMin); };
   // key groups that the tile of packed rows [r0, r0 + n) sees, without a window
   auto groups_of = [&](const StepSeq& s, int64_t r0, int64_t n) {
     return (s.start + (std::min<int64_t>(r0 + n, (int64_t)s.rows * G) - 1) / G) / kKvGroup + 1;

@@ -66,10 +66,10 @@ def test_weights_of_split_prompt_tiles_keep_their_bits(code):
     """Keys split over workgroups."""
     with KvCase(torch, "f16", code, 8, 2, 64, 64, max_seqs=1, max_tokens=3000) as c:
         c.append([0], [2400])
-        st, info, ws, q, starts = c.append([0], [20])
+        st, info, ws, q, starts = c.append([0], [24])
         assert info["n_prompt_tiles"] > 1 and info["workspace_bytes"] > 0
         out = c.attend(st, q, ws, 0.125)
-        weight_bits(c, out, q, [0], [20], starts, 0.125)
+        weight_bits(c, out, q, [0], [24], starts, 0.125)
 
 
 def natural(c, out, q, seqs, counts, starts, scale, window=0):
@@ -241,13 +241,13 @@ def test_prompts_that_fill_the_chip_once_and_more(code, seqs, rows, window):
 
 
 @pytest.mark.parametrize("code", CODES)
-@pytest.mark.parametrize("dim,heads,kv,block", [(128, 8, 2, 64), (256, 8, 2, 32), (128, 64, 1, 32)])
+@pytest.mark.parametrize("dim,heads,kv,block", [(128, 8, 2, 64), (256, 8, 2, 32), (128, 100, 1, 32)])
 @pytest.mark.parametrize("window", [0, 700, 10])
 def test_split_prompt_tiles_of_wide_heads(code, dim, heads, kv, block, window):
     """Keys split over workgroups and joined, also where a window leaves some of them nothing; and a single token whose
-    64 query heads share a kv head."""
+    100 query heads share a kv head."""
     with KvCase(torch, "f16", code, heads, kv, dim, block, max_seqs=2, max_tokens=2500) as c:
-        rows = [1, 1] if heads == 64 else [20, 13]
+        rows = [1, 1] if heads == 100 else [30, 25]
         c.append([0, 1], [2400, 1500])
         st, info, ws, q, starts = c.append([0, 1], rows)
         assert info["n_prompt_tiles"] > 2 and info["n_row_tiles"] == 0 and info["workspace_bytes"] > 0
@@ -265,3 +265,25 @@ def test_few_rows_after_a_long_context_fill_the_chip_with_splits(code):
         out = c.attend(st, q, ws, 0.09)
         part, heads = some_heads(c, [5])
         weight_bits(part, out[:, heads], q[:, heads], [0], [64], starts, 0.09)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("rows", [48, 130])
+def test_prompt_tiles_with_peaked_scores_and_a_row_of_nan(code, rows):
+    """Scores of some hundreds of both signs and none; a query row of NaN or infinity is alone.  48 rows of a fresh
+    prompt, 130 after 200 tokens with large values."""
+    with KvCase(torch, "f16", code, 4, 4, 64, 32) as c:
+        if rows == 130:
+            c.append([0], [200], 6.0)
+        st, info, ws, q, starts = c.append([0], [rows], 6.0, q=c.draw(rows, 4) * np.float16(6))
+        assert info["n_prompt_tiles"] and not info["n_row_tiles"]
+        for scale in (1.0, -0.5, 0.0):
+            clean = c.attend(st, q, ws, scale)
+            c.check_attend(clean, q, [0], [rows], starts, scale)
+            for bad in (float("nan"), float("inf")):
+                x = q.clone()
+                x[40, 2, 7] = bad
+                out = c.attend(st, x, ws, scale)
+                assert torch.isnan(out[40, 2]).all()
+                out[40, 2] = clean[40, 2]
+                assert torch.equal(out, clean)

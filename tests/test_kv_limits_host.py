@@ -120,3 +120,20 @@ def test_binding_knows_another_gpu():
         S.slora_kv_destroy(kv)
     finally:
         S.slora_pool_destroy(pool)
+
+
+@pytest.mark.parametrize("dtype", [S.SLORA_F16, S.SLORA_F32])
+@pytest.mark.parametrize("heads,before,rows,prompt", [(2, 0, 47, False), (2, 0, 48, True), (2, 10, 95, False),
+                                                      (2, 10, 96, True), (8, 100, 23, False), (8, 100, 24, True),
+                                                      (64, 100, 1, False), (192, 100, 1, True), (192, 0, 1, True)])
+def test_which_rows_take_prompt_tiles(dtype, heads, before, rows, prompt):
+    """96 packed rows of a kv head, or 48 of a fresh prompt, in fp16 pools; all others 16 at a time."""
+    with Cache(dtype=dtype, elems=4096, n_heads=heads, max_tokens=200, n_pages=200) as c:
+        if before:
+            c.step([0], [before])
+        info = S.slora_kv_step_get_info(c.step([0], [rows]))
+        packed = rows * heads // 2
+        if prompt and dtype == S.SLORA_F16:
+            assert info["n_prompt_tiles"] == -(-packed // 128) and info["n_row_tiles"] == 0
+        else:
+            assert info["n_prompt_tiles"] == 0 and info["n_row_tiles"] == -(-packed // 16)
