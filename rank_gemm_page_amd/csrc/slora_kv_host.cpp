@@ -115,6 +115,7 @@ struct slora_kv_step {
   std::vector<KvTile> prompts, tiles, combine;
   std::vector<KvPatch> patches;
   int32_t n_rows = 0, max_len = 0, n_small = 0;
+  int32_t n_positions = 0;         // one more than the rows' largest position
   int64_t n_new_pages = 0;
   int64_t n_parts = 0, n_row_parts = 0;   // slots of split tiles, those of row tiles first
   const char* dev = nullptr;
@@ -378,6 +379,7 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
       st->gens.push_back(s.gen);
       st->ends.push_back(blocks);
       st->max_len = std::max(st->max_len, (int32_t)end);
+      if (counts[i]) st->n_positions = std::max(st->n_positions, (int32_t)end);
       need += (blocks - s.blocks) * kv->per_block();
       patches += (blocks - s.entered) * kv->per_block();
       for (int32_t p = start; p < end; ++p) st->row_pos.push_back(p);
@@ -520,7 +522,7 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* st, int32_t laye
   if (kv->d.rot_dim) {
     if (!cos_sin || reinterpret_cast<uintptr_t>(cos_sin) & 15)
       return fail(SLORA_E_INVAL, f + ": cos_sin must be non-NULL and 16-byte aligned");
-    if (n_positions < st->max_len) return fail(SLORA_E_INVAL, f + ": cos_sin does not hold every position of the step");
+    if (n_positions < st->n_positions) return fail(SLORA_E_INVAL, f + ": cos_sin does not hold every position of the step");
   }
   if ((ok = check_order(f, kv, st, layer)) != SLORA_OK) return ok;
   if (!st->dev) return fail(SLORA_E_INVAL, f + ": step not uploaded (call slora_kv_step_upload)");

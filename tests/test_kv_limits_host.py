@@ -137,3 +137,15 @@ def test_which_rows_take_prompt_tiles(dtype, heads, before, rows, prompt):
             assert info["n_prompt_tiles"] == -(-packed // 128) and info["n_row_tiles"] == 0
         else:
             assert info["n_prompt_tiles"] == 0 and info["n_row_tiles"] == -(-packed // 16)
+
+
+def test_the_table_of_angles_holds_the_rows_positions_only():
+    """A sequence that gains nothing in a step needs no angles."""
+    with Cache() as c:
+        c.step([0], [90])
+        s = c.step([0, 1], [0, 5])
+        assert S.slora_kv_step_get_info(s)["max_len"] == 90
+        msg = refused(S.SLORA_E_INVAL, S.slora_kv_append, c.kv, s, 0, X, X, cos_sin=X, n_positions=4)
+        assert "position" in msg
+        msg = refused(S.SLORA_E_INVAL, S.slora_kv_append, c.kv, s, 0, X, X, cos_sin=X, n_positions=5)
+        assert "not uploaded" in msg
