@@ -627,6 +627,7 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* step, int32_t la
  *     s_j = scale * q[t, h] . k_j      out[t, h] = sum_j softmax(s)_j v_j
  *
  * over positions j <= p, with window > 0 also j > p - window (0: no window).
+ * scale * log2(e) must be finite in fp32, out must not overlap q.
  * k and v are the cached values; products are accumulated in fp32 (numbers below
  * 2^-126 may count as 0 there), the softmax
  * is held in fp32, and out is rounded once to the pool dtype.  q is [n_rows]

@@ -559,7 +559,8 @@ slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* st, int32_t laye
   const std::string f = "slora_kv_attend";
   slora_status ok = check_launch(f, kv, st, layer);
   if (ok != SLORA_OK) return ok;
-  if (!std::isfinite(scale)) return fail(SLORA_E_INVAL, f + ": scale must be finite");
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return fail(SLORA_E_INVAL, f + ": scale times log2(e) must be finite in fp32");
   if (window < 0) return fail(SLORA_E_INVAL, f + ": window must be 0 (none) or positive");
   if (st->n_rows == 0) return SLORA_OK;
   if (!q || !out) return fail(SLORA_E_INVAL, f + ": NULL q or out");
@@ -587,7 +588,7 @@ slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* st, int32_t laye
   A.out = out;
   A.q_stride = q_stride;
   A.out_stride = out_stride;
-  A.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  A.scale_log2 = scale_log2;
   A.part = static_cast<float*>(workspace);
   return launched(f, launch_kv_attend(A, static_cast<hipStream_t>(stream)));
 }

@@ -149,3 +149,12 @@ def test_the_table_of_angles_holds_the_rows_positions_only():
         assert "position" in msg
         msg = refused(S.SLORA_E_INVAL, S.slora_kv_append, c.kv, s, 0, X, X, cos_sin=X, n_positions=5)
         assert "not uploaded" in msg
+
+
+@pytest.mark.parametrize("scale", [3e38, -2.5e38, float("inf"), float("nan")])
+def test_scales_beyond_fp32_are_refused(scale):
+    """The kernels hold scale * log2(e): infinite, every score would be NaN."""
+    with Cache() as c:
+        s = c.step([0], [5])
+        assert "scale" in refused(S.SLORA_E_INVAL, S.slora_kv_attend, c.kv, s, 0, X, X, scale)
+        assert "not uploaded" in refused(S.SLORA_E_INVAL, S.slora_kv_attend, c.kv, s, 0, X, X, 2.3e38)
