@@ -25,11 +25,6 @@ constexpr int kKvPromptRows = 128;   // query rows of one prompt tile
 inline constexpr int64_t kv_k_byte(int slot, int d, int dim) {
   return (int64_t)(slot >> 4) * 16 * dim + (d >> 6) * 1024 + (slot & 15) * 64 + (d & 63);
 }
-inline constexpr int64_t kv_v_byte(int slot, int d, int dim) {
-  const int t = slot & 31;
-  return (int64_t)(slot >> 5) * 32 * dim + (d >> 5) * 1024 + ((t & 15) >> 2) * 256 + ((d & 31) >> 1) * 16 +
-         (d & 1) * 8 + (t >> 4) * 4 + (t & 3);
-}
 
 struct KvView {
   char* base;              // pages of the class

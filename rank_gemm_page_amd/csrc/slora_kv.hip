@@ -1137,7 +1137,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
 
 // Joins the splits of a prompt tile, 16 rows of it at a time: one workgroup per row.  D / 4 threads read a
 // split's row, so 1024 / D splits are read side by side and then joined in LDS.
-template <typename T, int D>
+template <int D>
 __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
   constexpr int TR = D / 4, NS = kThreads / TR;
   __shared__ float lds_o[NS][D];
@@ -1177,10 +1177,10 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
     ll += f * lds_l[s];
     o += f * *(const float4v*)&lds_o[s][d];
   }
-  T* out = (T*)A.out + (int64_t)(tile.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + d;
+  _Float16* out = (_Float16*)A.out + (int64_t)(tile.row0 + gr / G) * A.out_stride + (head * G + gr % G) * D + d;
   const float inv = 1.f / ll;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) out[j] = (T)(o[j] * inv);
+  for (int j = 0; j < 4; ++j) out[j] = (_Float16)(o[j] * inv);
 }
 
 // ---------------------------------------------------------------------------
@@ -1316,10 +1316,9 @@ static const void* prompt_of(int dim, bool triple) {
          : dim == 256 ? (const void*)kv_attend_prompt_kernel<CODE, 256, false>
          : triple ? (const void*)kv_attend_prompt_kernel<CODE, 128, true> : (const void*)kv_attend_prompt_kernel<CODE, 128, false>;
 }
-template <typename T>
 static const void* combine_of(int dim) {
-  return dim == 64 ? (const void*)kv_combine_kernel<T, 64>
-         : dim == 128 ? (const void*)kv_combine_kernel<T, 128> : (const void*)kv_combine_kernel<T, 256>;
+  return dim == 64 ? (const void*)kv_combine_kernel<64>
+         : dim == 128 ? (const void*)kv_combine_kernel<128> : (const void*)kv_combine_kernel<256>;
 }
 
 hipError_t launch_kv_append(const KvAppend& A0, hipStream_t stream) {
@@ -1356,8 +1355,7 @@ hipError_t launch_kv_attend(const KvAttend& A, hipStream_t stream) {
   e = run(half ? rows_of<_Float16>(A.kv.code, A.kv.dim) : rows_of<float>(A.kv.code, A.kv.dim),
                      (int64_t)A.n_tiles * A.kv.n_kv, A, stream);
   if (e != hipSuccess) return e;
-  return run(half ? combine_of<_Float16>(A.kv.dim) : combine_of<float>(A.kv.dim), (int64_t)A.n_combine * A.kv.n_kv * kKvRows,
-             A, stream);
+  return run(combine_of(A.kv.dim), (int64_t)A.n_combine * A.kv.n_kv * kKvRows, A, stream);
 }
 
 hipError_t launch_kv_read(const KvRead& R, hipStream_t stream) {
