@@ -492,12 +492,13 @@ const char* slora_last_error(void);
  *     code * range / 448   (SLORA_KV_FP8: code = an e4m3 number)
  *
  * and is the nearest one to the appended value (ties to even), computed in 64
- * bits as value * (127 or 448 / range); a range is rounded to fp32, and where it
- * is subnormal a value that passes it takes the last code.  When a later append raises the range
- * of a block that is partly filled, its older codes are coded again:
- * nearest(code * (old range / new range)).  A value that is not finite (or,
- * after the rotation, beyond fp32) makes the range NaN, and every key (or
- * value) of that block and head then reads as NaN: it is never lost silently.
+ * bits as value * (127 or 448 / range); for e4m3 the product is rounded to fp32
+ * first.  A range is rounded to fp32, and where it is subnormal a value that
+ * passes it takes the last code.  When a later append raises the range of a block
+ * that is partly filled, its older codes are coded again: nearest(code * (old
+ * range / new range)).  A value that is not finite (or, after the rotation,
+ * beyond fp32) makes the range NaN, and every key (or value) of that block and
+ * head then reads as NaN: it is never lost silently.
  *
  * Position p of a sequence is its p-th token (0, 1, ...).  Rotation by
  * positions: for the pairs (a_i, b_i), i = 0 .. rot_dim/2 - 1, of a head,
@@ -507,8 +508,9 @@ const char* slora_last_error(void);
  * pairs are (i, i + rot_dim/2) (SLORA_KV_HALVES) or (2i, 2i + 1)
  * (SLORA_KV_NEIGHBOURS); elements from rot_dim on stay as they are.  Keys are
  * rotated in 64 bits before they are coded, q in fp32 (a product and the sum
- * rounded once each) and rounded to the pool dtype.  cos_sin is the caller's table, device fp32 [n_positions][rot_dim]: a
- * position's rot_dim/2 cosines, then its rot_dim/2 sines.
+ * rounded once each) and rounded to the pool dtype.  cos_sin is the caller's
+ * table, device fp32 [n_positions][rot_dim]: a position's rot_dim/2 cosines, then
+ * its rot_dim/2 sines.
  *
  * One step of a server: slora_kv_build_step names the sequences of the batch
  * and how many tokens each one gains, slora_kv_step_upload brings the step to

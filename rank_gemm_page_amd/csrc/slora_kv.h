@@ -35,7 +35,8 @@ struct KvView {
 };
 
 // Records of a step (device metadata, int32 words).
-struct KvBlock { int32_t seq, block, slot0, slot1, row, pad[3]; };   // sequence id, block, its slots [slot0, slot1) among the rows, batch row of slot0
+// A touched block: sequence id, block, its slots [slot0, slot1) among the rows, batch row of slot0.
+struct KvBlock { int32_t seq, block, slot0, slot1, row, pad[3]; };
 // A tile of a sequence's packed rows: number, key split of how many, slots (see below); and the sequence: its first
 // row's position, its rows, the batch row of the first.
 struct KvTile { int32_t seq, tile, split, splits, part, start, rows, row0; };

@@ -70,7 +70,8 @@ template <> struct Code<SLORA_KV_FP8> {
   static __device__ __forceinline__ float value(uint32_t byte) {
     return __builtin_amdgcn_cvt_pk_f32_fp8((int)byte, false)[0];
   }
-  // The definition rounds the 64-bit product to fp32 and then to e4m3.
+  // The definition rounds the 64-bit product to fp32 and then to e4m3.  A
+  // subnormal range's values are held at the last code as above.
   static __device__ __forceinline__ uint32_t nearest(double x) {
     const float y = __builtin_amdgcn_fmed3f((float)x, -kTop, kTop);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, 0.f, 0, false) & 0xFF;
@@ -124,7 +125,8 @@ __device__ __forceinline__ Pairs<T> load_pairs(const KvView& kv, const T* head, 
   typedef typename Vec<T>::v8 V;
   const V x = *reinterpret_cast<const V*>(head + a), y = *reinterpret_cast<const V*>(head + b);
   if (kv.pairs == SLORA_KV_HALVES) return {x, y};
-  return {__builtin_shufflevector(x, y, 0, 2, 4, 6, 8, 10, 12, 14), __builtin_shufflevector(x, y, 1, 3, 5, 7, 9, 11, 13, 15)};
+  return {__builtin_shufflevector(x, y, 0, 2, 4, 6, 8, 10, 12, 14),
+          __builtin_shufflevector(x, y, 1, 3, 5, 7, 9, 11, 13, 15)};
 }
 __device__ __forceinline__ Turn load_turn(const KvView& kv, const float* cos_sin, int64_t pos, int u) {
   if (u * 16 >= kv.rot) return {float8v{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, float8v{}};
@@ -186,16 +188,19 @@ template <int CODE>
 __device__ __forceinline__ uint32_t again4(uint32_t old, double ratio) {
   uint32_t w = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w |= Code<CODE>::nearest((double)Code<CODE>::value((old >> (8 * j)) & 0xFF) * ratio) << (8 * j);
+  for (int j = 0; j < 4; ++j)
+    w |= Code<CODE>::nearest((double)Code<CODE>::value((old >> (8 * j)) & 0xFF) * ratio) << (8 * j);
   return w;
 }
 template <int CODE>
 __device__ __forceinline__ uint4 again16(uint4 o, double ratio) {
-  return make_uint4(again4<CODE>(o.x, ratio), again4<CODE>(o.y, ratio), again4<CODE>(o.z, ratio), again4<CODE>(o.w, ratio));
+  return make_uint4(again4<CODE>(o.x, ratio), again4<CODE>(o.y, ratio), again4<CODE>(o.z, ratio),
+                    again4<CODE>(o.w, ratio));
 }
 
-// Elements of a value unit as they are read: 8 of each of two tokens.  old: the unit as the page holds it, where the append leaves some of its
-// tokens as they are.
+// Elements of a value unit as they are read: 8 of each of two tokens.  old: the
+// unit as the page holds it, where the append leaves some of its tokens as they
+// are.
 template <typename T> struct Values { typename Vec<T>::v8 x[2]; uint4 old; };
 
 // What both kinds of item need.
@@ -354,8 +359,10 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
     }
     uint2 first = make_uint2(wa[0], wa[1]), second = make_uint2(wb[0], wb[1]);
     if (kv.pairs == SLORA_KV_NEIGHBOURS) {
-      first = make_uint2(__builtin_amdgcn_perm(wb[0], wa[0], 0x05010400u), __builtin_amdgcn_perm(wb[0], wa[0], 0x07030602u));
-      second = make_uint2(__builtin_amdgcn_perm(wb[1], wa[1], 0x05010400u), __builtin_amdgcn_perm(wb[1], wa[1], 0x07030602u));
+      first = make_uint2(__builtin_amdgcn_perm(wb[0], wa[0], 0x05010400u),
+                         __builtin_amdgcn_perm(wb[0], wa[0], 0x07030602u));
+      second = make_uint2(__builtin_amdgcn_perm(wb[1], wa[1], 0x05010400u),
+                          __builtin_amdgcn_perm(wb[1], wa[1], 0x07030602u));
     }
     if (bad) first = second = make_uint2(C::kZero * 0x01010101u, C::kZero * 0x01010101u);
     *reinterpret_cast<uint2*>(it.page + kv_k_byte(slot, a, it.dim)) = first;
@@ -395,7 +402,8 @@ __device__ __forceinline__ void store_values(const KvAppend& A, uint32_t at, int
   auto load = [&](int u, Values<T>* x) {
     const int group = group0 + (u >> (ush + 5)), e = (u >> 6) & ((1 << (ush - 1)) - 1);
     x->old = make_uint4(0, 0, 0, 0);
-    if (group * 32 < blk.slot0 || group * 32 + 32 > blk.slot1) x->old = ld16(base + (int64_t)(group0 * it.dim * 2 + u) * 16);
+    if (group * 32 < blk.slot0 || group * 32 + 32 > blk.slot1)
+      x->old = ld16(base + (int64_t)(group0 * it.dim * 2 + u) * 16);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int slot = group * 32 + h * 16 + g * 4 + k4;
@@ -537,7 +545,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
 // Of 16 rows a single token fills only G; the matrix cores have ten times what
 // HBM can feed that way, and a vector dot product would spend its instructions
 // on the conversions alone.  256 requests of 300 to 2000 tokens, 32 heads: 350 us,
-// 6.5 TB/s of codes (the largest copy runs at 5.2, reads alone at up to 6.6).
+// 6.5 TB/s of codes (the largest copy runs at 5.2, reads alone at up to 6.6); 32
+// heads of 64 187 us (6.1), 16 of 256 346 us (6.6).
 
 template <typename T> struct Frag;
 template <> struct Frag<_Float16> { typedef half8 type; };
@@ -548,7 +557,9 @@ template <> struct Frag<float> { typedef float8v type; };
 template <int CODE>
 __device__ __forceinline__ void codes8(uint32_t a, uint32_t b, float, half8* r) { *r = Code<CODE>::halves(a, b); }
 template <int CODE>
-__device__ __forceinline__ void codes8(uint32_t a, uint32_t b, float unit, float8v* r) { *r = floats8<CODE>(a, b) * unit; }
+__device__ __forceinline__ void codes8(uint32_t a, uint32_t b, float unit, float8v* r) {
+  *r = floats8<CODE>(a, b) * unit;
+}
 
 __device__ __forceinline__ float4v mma(half8 a, half8 b, float4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -611,7 +622,8 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, int splits, uint32_t*
 // The bound of two waves a SIMD makes the compiler spare registers: three run at
 // heads of 128 (147 registers instead of 184, decode batch 374 to 350 us) and five
 // at 64.  Heads of 256 reach two by loading the next keys only when these are
-// multiplied (f16 324 to 194 registers, 9000 tokens on 4 kv heads 88 to 61 us).
+// multiplied (f16 324 to 194 registers, 16 requests of 4500 to 9000 tokens, 16
+// heads on 4, 88 to 59 us).
 template <typename T, int CODE, int D>
 __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A) {
   using F = typename Frag<T>::type;
@@ -808,7 +820,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
   l += __shfl_xor(l, 32);
   if (g == 0) { lds_ml[wave][i][0] = m; lds_ml[wave][i][1] = l; }
   if (lane == 0) lds_ref[wave] = values ? 1.f : ref / Code<CODE>::kTop;
-  float* part = tile.splits > 1 ? A.part + ((int64_t)(tile.part + tile.split) * kv.n_kv + head) * kv_part_floats(D) : nullptr;
+  float* part = tile.splits > 1
+                    ? A.part + ((int64_t)(tile.part + tile.split) * kv.n_kv + head) * kv_part_floats(D) : nullptr;
   constexpr int PER = DC / 16;                   // columns of a thread
   const int orow = tid >> 4, od = (tid & 15) * PER, gr = tile.tile * kKvRows + orow;
 #pragma unroll
@@ -930,7 +943,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
   const int w_lo = A.window ? max(0, w_first - A.window + 1) : 0, w_all = A.window ? max(0, w_last - A.window + 1) : 0;
   half8 qf[KS];
   {
-    const _Float16* q = (const _Float16*)A.q + (int64_t)(tile.row0 + pos - tile.start) * A.q_stride + (head * G + rr % G) * D;
+    const _Float16* q =
+        (const _Float16*)A.q + (int64_t)(tile.row0 + pos - tile.start) * A.q_stride + (head * G + rr % G) * D;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       qf[k] = *(const half8*)(q + k * 16 + h * 8);
@@ -1051,7 +1065,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
       }
       // values of a block count in units of its range: sums are kept in units of
       // a reference range, replaced when a block's is far from it.  The weights
-      // carry the factor in their exponent, and their sum is freed of it.
+      // carry the factor in their exponent, and their sum is freed of it; the
+      // approximate reciprocal and logarithm weigh the block wrongly by 2^-20, where
+      // the output has 11 bits.
       float unit = 1.f;
       if (rv[x] > 0.f) {
         unit = rv[x] * __builtin_amdgcn_rcpf(ref);
@@ -1066,8 +1082,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
       const float shift = __builtin_amdgcn_logf(unit) - m;
       // each weight as the sum of two fp16 numbers, as in the row tiles: with one,
       // the error against 64 bits was 1.1 to 1.35 times that of the output's own
-      // rounding.  The rest of a weight is one mixed-precision fma, for which the
-      // factor -1 must not look like a constant.
+      // rounding.  The second product costs 547 to 700 us for 2048 tokens after
+      // 6001 and 78 to 88 us for 32 prompts, wherever it is placed among the other
+      // instructions.  The rest of a weight is one mixed-precision fma, for which
+      // the factor -1 must not look like a constant.
       float sum = 0.f;
 #pragma unroll
       for (int tt = 0; tt < 2; ++tt) {
@@ -1188,9 +1206,10 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttend A) {
 // elements of a token from K, and a 16-byte unit of V, turned across four lanes
 // into 8 elements of each of two tokens, so that stores are 16 bytes a lane and
 // 64 bytes or more a run.  Nothing here reads them again: non-temporal stores
-// took 8 sequences of up to 4000 tokens from 22.0 to 18.2 us (5.1 TB/s).  fp32
-// rows are stored in two halves of every 32 bytes, which such stores do not
-// merge (3.2 TB/s against 4.6).
+// took 8 sequences of up to 4000 tokens from 22.0 to 18.2 us (now 17.8, 5.2 TB/s).
+// fp32 rows are stored in two halves of every 32 bytes, which such stores do not
+// merge (3.2 TB/s against 4.6 when both were tried); the same sequences in fp32 take
+// 37 us (4.2 TB/s).
 
 // Fp32 values are multiplied in 64 bits, where the unit of a small range is as
 // exact as any: in fp32, ranges below 127 times the smallest number read as 0.
@@ -1304,7 +1323,8 @@ static const void* read_of(int code) {
 template <typename T, int CODE>
 static const void* rows_of(int dim) {
   return dim == 64 ? (const void*)kv_attend_rows_kernel<T, CODE, 64>
-         : dim == 128 ? (const void*)kv_attend_rows_kernel<T, CODE, 128> : (const void*)kv_attend_rows_kernel<T, CODE, 256>;
+         : dim == 128 ? (const void*)kv_attend_rows_kernel<T, CODE, 128>
+                      : (const void*)kv_attend_rows_kernel<T, CODE, 256>;
 }
 template <typename T>
 static const void* rows_of(int code, int dim) {
@@ -1314,7 +1334,8 @@ template <int CODE>
 static const void* prompt_of(int dim, bool triple) {
   return dim == 64 ? (const void*)kv_attend_prompt_kernel<CODE, 64, false>
          : dim == 256 ? (const void*)kv_attend_prompt_kernel<CODE, 256, false>
-         : triple ? (const void*)kv_attend_prompt_kernel<CODE, 128, true> : (const void*)kv_attend_prompt_kernel<CODE, 128, false>;
+         : triple ? (const void*)kv_attend_prompt_kernel<CODE, 128, true>
+                  : (const void*)kv_attend_prompt_kernel<CODE, 128, false>;
 }
 static const void* combine_of(int dim) {
   return dim == 64 ? (const void*)kv_combine_kernel<64>
@@ -1332,7 +1353,8 @@ hipError_t launch_kv_append(const KvAppend& A0, hipStream_t stream) {
   // workgroup b has q workgroups floor(b * share / 2^32) before it: with the
   // share rounded up, exactly q of all (there is always an item: q < all)
   A.q_share = (uint32_t)((((uint64_t)q << 32) + (uint64_t)(q + items) - 1) / (uint64_t)(q + items));
-  return run(A.kv.dtype == SLORA_F16 ? append_of<_Float16>(A.kv.code) : append_of<float>(A.kv.code), q + items, A, stream);
+  return run(A.kv.dtype == SLORA_F16 ? append_of<_Float16>(A.kv.code) : append_of<float>(A.kv.code), q + items, A,
+             stream);
 }
 
 hipError_t launch_kv_attend(const KvAttend& A, hipStream_t stream) {

@@ -47,7 +47,8 @@ const char* check_desc(const slora_pool* pool, const slora_kv_desc* d, PoolInfo*
   if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return "head_dim must be 64, 128 or 256";
   if (d->max_seqs < 1 || d->max_tokens < 1) return "max_seqs and max_tokens must be positive";
   if (d->max_tokens > (1 << 30)) return "max_tokens must be at most 2^30";
-  if (d->rot_dim < 0 || d->rot_dim > d->head_dim || d->rot_dim % 16) return "rot_dim must be a multiple of 16 up to head_dim";
+  if (d->rot_dim < 0 || d->rot_dim > d->head_dim || d->rot_dim % 16)
+    return "rot_dim must be a multiple of 16 up to head_dim";
   if (d->rot_pairs != SLORA_KV_HALVES && d->rot_pairs != SLORA_KV_NEIGHBOURS)
     return "rot_pairs must be SLORA_KV_HALVES or SLORA_KV_NEIGHBOURS";
   if (d->reserved0 != 0) return "reserved0 must be 0";
@@ -127,16 +128,22 @@ struct slora_kv_step {
   size_t row_pos_off() const { return patches_off() + patches.size() * sizeof(KvPatch); }
   size_t counters_off() const { return row_pos_off() + row_pos.size() * sizeof(int32_t); }
   size_t bytes() const { return counters_off() + (size_t)n_row_parts * kv->d.n_kv_heads * sizeof(uint32_t); }
-  size_t workspace() const { return (size_t)n_parts * kv->d.n_kv_heads * kv_part_floats(kv->d.head_dim) * sizeof(float); }
+  size_t workspace() const {
+    return (size_t)n_parts * kv->d.n_kv_heads * kv_part_floats(kv->d.head_dim) * sizeof(float);
+  }
 };
 
 namespace {
 
 // Row tiles: key groups of 32 a workgroup takes at least, and the workgroups a
-// launch is split into at most.  Fewer than 8 groups bring nothing (one token
-// after 777: 10 us with 4, 8 and 16); 1536 workgroups fill the places of the
-// chip, three a CU for heads of 128, twice (12 long conversations: 108 us, 110
-// with 2048, 120 with 3840).
+// launch is split into at most.  us with at least 4 | 8 | 16 groups: one token
+// after 777, 64 heads of 128 on 8, 8.1 | 7.9 | 9.7, 16 fp32 heads of 128 10.4 |
+// 12.6 | 20.4; one after 32000 51 | 42 | 29, where the join of the splits counts.
+// us with at most 1024 | 1536 | 2560 | 3840 workgroups, which is 1.3 to 5 times
+// the places of the chip for heads of 128: 12 conversations of 12000 to 33000
+// tokens, heads of 64 55 | 60 | 62 | 65, of 128 108 | 109 | 112 | 120, of 256 199 |
+// 205 | 214 | 227; 32 requests of 1000 to 3000, 32 heads on 8, of 64 18 | 20 | 21 |
+// 21, of 128 32 | 33 | 35 | 35, of 256 56 | 60 | 64 | 64.
 constexpr int64_t kMinGroups = 8, kWantGroups = 1536;
 
 // Sequences with at least kPromptMin packed rows (query heads of a kv head times
@@ -167,7 +174,8 @@ void build_tiles(slora_kv_step* st) {
   // groups of a workgroup: the fewest for which all row tiles' workgroups are at most kWantGroups
   std::vector<int64_t> lens;
   for (const StepSeq& s : st->seqs)
-    for (int64_t r0 = 0; !prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvRows) lens.push_back(groups_of(s, r0, kKvRows));
+    for (int64_t r0 = 0; !prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvRows)
+      lens.push_back(groups_of(s, r0, kKvRows));
   int64_t chunk = kMinGroups;
   if (!lens.empty()) {
     int64_t high = std::max(chunk, *std::max_element(lens.begin(), lens.end()));
@@ -202,7 +210,8 @@ void build_tiles(slora_kv_step* st) {
 
   int64_t total = 0;
   for (const StepSeq& s : st->seqs)
-    for (int64_t r0 = 0; prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvPromptRows) total += groups_of(s, r0, kKvPromptRows);
+    for (int64_t r0 = 0; prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvPromptRows)
+      total += groups_of(s, r0, kKvPromptRows);
   const int64_t most = std::max<int64_t>(kPromptGroups, (total * d.n_kv_heads + kWantPrompts - 1) / kWantPrompts);
   constexpr int32_t kRuns = kKvPromptRows / kKvRows;
   for (const StepSeq& s : st->seqs) {
@@ -230,7 +239,8 @@ slora_status check_launch(const std::string& f, const slora_kv* kv, const slora_
   if (layer < 0 || layer >= kv->d.n_layers) return fail(SLORA_E_INVAL, f + ": layer out of range");
   for (size_t i = 0; i < st->seqs.size(); ++i)
     if (kv->seqs[st->seqs[i].seq].gen != st->gens[i])
-      return fail(SLORA_E_STALE, f + ": sequence " + std::to_string(st->seqs[i].seq) + " was dropped since the step was built");
+      return fail(SLORA_E_STALE,
+                  f + ": sequence " + std::to_string(st->seqs[i].seq) + " was dropped since the step was built");
   return SLORA_OK;
 }
 
@@ -239,7 +249,8 @@ slora_status check_rows(const std::string& f, const char* name, const slora_kv* 
                         int32_t heads) {
   if (reinterpret_cast<uintptr_t>(p) & 15) return fail(SLORA_E_INVAL, f + ": " + name + " must be 16-byte aligned");
   if (stride < (int64_t)heads * kv->d.head_dim || stride * kv->elem() % 16 || stride > ((int64_t)1 << 40))
-    return fail(SLORA_E_INVAL, f + ": the stride of " + name + " must be at least heads * head_dim and a multiple of 16 bytes");
+    return fail(SLORA_E_INVAL,
+                f + ": the stride of " + name + " must be at least heads * head_dim and a multiple of 16 bytes");
   return SLORA_OK;
 }
 
@@ -347,18 +358,21 @@ slora_status slora_kv_pages(const slora_kv* kv, int32_t seq, int32_t layer, int3
 
 slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, const int32_t* counts, int32_t reread,
                                  slora_kv_step** out) {
-  if (!kv || !out || n < 0 || (n > 0 && (!seqs || !counts))) return fail(SLORA_E_INVAL, "slora_kv_build_step: NULL argument");
+  if (!kv || !out || n < 0 || (n > 0 && (!seqs || !counts)))
+    return fail(SLORA_E_INVAL, "slora_kv_build_step: NULL argument");
   if (reread != 0 && reread != 1) return fail(SLORA_E_INVAL, "slora_kv_build_step: reread must be 0 or 1");
   slora_kv_step* st = nullptr;
   try {
     std::vector<uint8_t> named((size_t)kv->d.max_seqs, 0);
     int64_t rows = 0;
     for (int32_t i = 0; i < n; ++i) {
-      if (seqs[i] < 0 || seqs[i] >= kv->d.max_seqs) return fail(SLORA_E_INVAL, "slora_kv_build_step: sequence id out of range");
+      if (seqs[i] < 0 || seqs[i] >= kv->d.max_seqs)
+        return fail(SLORA_E_INVAL, "slora_kv_build_step: sequence id out of range");
       if (named[seqs[i]]++) return fail(SLORA_E_INVAL, "slora_kv_build_step: a sequence is named twice");
       const int64_t len = kv->seqs[seqs[i]].len;
       if (counts[i] < 0) return fail(SLORA_E_INVAL, "slora_kv_build_step: negative count");
-      if (reread && counts[i] > len) return fail(SLORA_E_INVAL, "slora_kv_build_step: more rows than the sequence has tokens");
+      if (reread && counts[i] > len)
+        return fail(SLORA_E_INVAL, "slora_kv_build_step: more rows than the sequence has tokens");
       if (!reread && len + counts[i] > kv->d.max_tokens)
         return fail(SLORA_E_INVAL, "slora_kv_build_step: a sequence would pass max_tokens");
       rows += counts[i];
@@ -396,7 +410,8 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
     // a launch holds fewer than 2^32 threads, and counts in the kernels are 31 bits
     constexpr int64_t kMostGroups = ((int64_t)1 << 32) / kThreads - 1;
     const int64_t kvh = kv->d.n_kv_heads;
-    const int64_t append = 2 * (int64_t)st->blocks.size() * kvh + (rows * kv->d.n_heads * (kv->d.head_dim / 16)) / kThreads + 1;
+    const int64_t append =
+        2 * (int64_t)st->blocks.size() * kvh + (rows * kv->d.n_heads * (kv->d.head_dim / 16)) / kThreads + 1;
     if (std::max({append, (int64_t)st->prompts.size() * kvh, (int64_t)st->tiles.size() * kvh,
                   (int64_t)st->combine.size() * kvh * kKvRows}) > kMostGroups ||
         patches > INT32_MAX / 2 || rows * kv->d.n_heads > INT32_MAX / 2 || st->n_parts * kvh > INT32_MAX / 2) {
@@ -434,7 +449,8 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
       for (int32_t b = s.entered; b < s.blocks; ++b)
         for (int64_t x = 0; x < kv->per_block(); ++x) {
           const uint64_t entry = ((uint64_t)seqs[i] * kv->per_block() + x) * kv->max_blocks + b;
-          st->patches.push_back({(uint32_t)entry, (uint32_t)(entry >> 32), s.pages[(size_t)(b * kv->per_block() + x)], 0});
+          const int32_t page = s.pages[(size_t)(b * kv->per_block() + x)];
+          st->patches.push_back({(uint32_t)entry, (uint32_t)(entry >> 32), page, 0});
         }
     }
   } catch (const std::bad_alloc&) {
@@ -522,7 +538,8 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* st, int32_t laye
   if (kv->d.rot_dim) {
     if (!cos_sin || reinterpret_cast<uintptr_t>(cos_sin) & 15)
       return fail(SLORA_E_INVAL, f + ": cos_sin must be non-NULL and 16-byte aligned");
-    if (n_positions < st->n_positions) return fail(SLORA_E_INVAL, f + ": cos_sin does not hold every position of the step");
+    if (n_positions < st->n_positions)
+      return fail(SLORA_E_INVAL, f + ": cos_sin does not hold every position of the step");
   }
   if ((ok = check_order(f, kv, st, layer)) != SLORA_OK) return ok;
   if (!st->dev) return fail(SLORA_E_INVAL, f + ": step not uploaded (call slora_kv_step_upload)");

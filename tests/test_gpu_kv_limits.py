@@ -229,7 +229,7 @@ def some_heads(c, kv_heads):
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("seqs,rows,window", [(1, 300, 0), (3, 300, 0), (3, 300, 90), (5, 280, 0), (6, 300, 0)])
 def test_prompts_that_fill_the_chip_once_and_more(code, seqs, rows, window):
-    """192 to 1152 workgroups of 64 heads of 128: both forms of the prompt kernel, one round of its places and several."""
+    """192 to 1152 workgroups of 64 heads of 128: both forms of the prompt kernel, one round of its places and more."""
     with KvCase(torch, "f16", code, 64, 64, 128, 32, max_seqs=6, max_tokens=400) as c:
         ids = list(range(seqs))
         c.append(ids, [17 * i for i in ids])
