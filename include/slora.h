@@ -623,6 +623,62 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* step, int32_t la
                              int64_t k_stride, const void* v, int64_t v_stride, const float* cos_sin,
                              int64_t n_positions, void* stream);
 
+/* slora_kv_append for models that norm q and k head by head before the rotation:
+ * in every row and head, with x the head's head_dim elements,
+ *
+ *     x_i' = x_i / sqrt(mean_j x_j^2 + eps) * w_i
+ *
+ * k is normed in 64 bits (as it is rotated there), q in fp32 (in fp32 pools in 64
+ * bits, and rounded to fp32 before the rotation).  q_weight and k_weight are
+ * device memory of the pool dtype, 16-byte aligned: head_dim elements for all
+ * heads, or, with per_head, n_heads (n_kv_heads) times head_dim; NULL: ones.
+ * v is stored as it is.  eps is at least 2^-126 and finite. */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  int32_t per_head;     /* 0 or 1 */
+} slora_kv_norm;
+slora_status slora_kv_append_norm(slora_kv* kv, const slora_kv_step* step, int32_t layer, const void* q,
+                                  int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride, const slora_kv_norm* norm,
+                                  const float* cos_sin, int64_t n_positions, void* stream);
+
+/* The table of cosines and sines that append takes, for positions first ..
+ * first + n - 1 (up to 2^30): row p - first holds amplitude * cos(p f_i), i = 0 ..
+ * rot_dim/2 - 1, then amplitude * sin(p f_i), each from 64 bits and rounded once.
+ * With t_i = base^(-2i / rot_dim) the frequencies are
+ *
+ *   SLORA_KV_ROT_NONE    f_i = t_i
+ *   SLORA_KV_ROT_LINEAR  f_i = t_i / factor
+ *   SLORA_KV_ROT_BASE    f_i = t_i with base * factor^(rot_dim / (rot_dim - 2)) as the base
+ *   SLORA_KV_ROT_BANDS   f_i = t_i (s + (1 - s) / factor), s = (turns_i - low) / (high - low)
+ *                        held in 0 .. 1, turns_i = trained t_i / (2 pi): pairs that turn
+ *                        often over the trained length keep their frequency
+ *   SLORA_KV_ROT_RAMP    f_i = t_i (1 - r + r / factor), r = (i - i_high) / (i_low - i_high)
+ *                        held in 0 .. 1, i_low and i_high the pairs that would make low
+ *                        and high turns over the trained length, rot_dim ln(trained / (2 pi
+ *                        turns)) / (2 ln base): i_low rounded up and at most rot_dim - 1,
+ *                        i_high down and at least 0, and at least 0.001 apart
+ *
+ * base > 1, factor >= 1, trained >= 1, 0 < low < high (the last three only where
+ * they are used) and amplitude are finite.  cos_sin is device memory, fp32 [n][rot_dim],
+ * 16-byte aligned.  One launch on `stream`; refused where rot_dim is 0. */
+typedef enum {
+  SLORA_KV_ROT_NONE = 0,
+  SLORA_KV_ROT_LINEAR = 1,
+  SLORA_KV_ROT_BASE = 2,
+  SLORA_KV_ROT_BANDS = 3,
+  SLORA_KV_ROT_RAMP = 4
+} slora_kv_rot_scaling;
+typedef struct {
+  int32_t scaling;      /* slora_kv_rot_scaling */
+  int32_t reserved0;    /* must be 0 */
+  double base, factor, trained, low, high, amplitude;
+} slora_kv_rotary;
+slora_status slora_kv_rotary_table(slora_kv* kv, const slora_kv_rotary* rotary, int64_t first, int64_t n,
+                                   float* cos_sin, void* stream);
+
 /* Attention of the step's rows in `layer` over the cached tokens: for row t at
  * position p of its sequence and query head h,
  *

@@ -32,6 +32,41 @@ def angles(n_positions, rot, base=10000.0):
     return np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float32)
 
 
+def frequencies(rot, base=10000.0, scaling="none", factor=1.0, trained=0.0, low=0.0, high=0.0):
+    """Angle per position of each pair, in numpy's longest floating type."""
+    wide = np.longdouble
+    i = np.arange(rot // 2).astype(wide)
+    base, two_pi = wide(base), 8 * np.arctan(wide(1))
+    if scaling == "base":
+        base = base * wide(factor) ** (wide(rot) / (rot - 2))
+    t = base ** (-2 * i / rot)
+    if scaling in ("none", "base"):
+        return t
+    if scaling == "linear":
+        return t / factor
+    if scaling == "bands":
+        s = np.clip((trained * t / two_pi - low) / (wide(high) - low), 0, 1)
+        return t * (s + (1 - s) / factor)
+    pair = [rot * np.log(trained / (two_pi * turns)) / (2 * np.log(base)) for turns in (low, high)]
+    i_low, i_high = min(np.ceil(pair[0]), rot - 1), max(np.floor(pair[1]), 0)
+    r = np.clip((i - i_high) / max(i_low - i_high, wide(0.001)), 0, 1)
+    return t * (1 - r + r / factor)
+
+
+def rotary_table(first, n, rot, amplitude=1.0, **scaling):
+    """64-bit table [n, rot] of positions first .. first + n - 1: cosines, then sines."""
+    a = (np.arange(n).astype(np.longdouble) + first)[:, None] * frequencies(rot, **scaling)
+    return np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float64) * amplitude
+
+
+def normed(x, weight=None, eps=1e-6):
+    """Each head [..., dim] over the root of its mean square, times its weights, in 64 bits."""
+    x = np.asarray(x, np.float64)
+    with np.errstate(invalid="ignore"):
+        y = x / np.sqrt(np.mean(x * x, -1, keepdims=True) + eps)
+        return y if weight is None else y * np.asarray(weight, np.float64)
+
+
 def rotate(x, cs, rot, pairs):
     """x [n, heads, dim] rotated by the rows of cs [n, rot], in 64 bits."""
     y = np.array(x, np.float64)

@@ -59,6 +59,11 @@ struct KvAppend {
   int64_t q_stride, q_out_stride, k_stride, v_stride;
   const float* cos_sin;
   const int32_t* row_pos;     // [n_rows] position of every row
+  // the norms of q and k, where they have any: weights (NULL: ones) of all heads,
+  // or those of head h at h * w_stride
+  const void* q_weight; const void* k_weight;
+  float eps;
+  int32_t w_stride;           // 0 or head_dim
 };
 
 struct KvAttend {
@@ -82,8 +87,18 @@ struct KvRead {
   int64_t k_stride, v_stride;
 };
 
+// Table of cosines and sines: pair i turns by turn_hi[i] + turn_lo[i] full turns a position.
+struct KvRotary {
+  double turn_hi[128], turn_lo[128];
+  double amplitude;
+  float* out;                 // [n][2 * half]
+  int64_t first, n;
+  int32_t half, run;          // run: positions of a thread
+};
+
+hipError_t launch_kv_rotary(const KvRotary& R, hipStream_t stream);
 hipError_t launch_kv_patch(int32_t* table, const KvPatch* patches, int32_t n, hipStream_t stream);
-hipError_t launch_kv_append(const KvAppend& A, hipStream_t stream);
+hipError_t launch_kv_append(const KvAppend& A, bool norm, hipStream_t stream);
 hipError_t launch_kv_attend(const KvAttend& A, hipStream_t stream);
 hipError_t launch_kv_read(const KvRead& R, hipStream_t stream);
 

@@ -135,9 +135,9 @@ __device__ __forceinline__ Turn load_turn(const KvView& kv, const float* cos_sin
 }
 // Products of an fp16 or fp32 element and an fp32 cosine are exact in 64 bits,
 // so the result is rounded once whether or not the compiler fuses them.
-__device__ __forceinline__ void turned(float a, float b, float c, float s, double* ra, double* rb) {
-  *ra = (double)a * c - (double)b * s;
-  *rb = (double)b * c + (double)a * s;
+__device__ __forceinline__ void turned(double a, double b, float c, float s, double* ra, double* rb) {
+  *ra = a * c - b * s;
+  *rb = b * c + a * s;
 }
 
 // The same in fp32: one rounding of a product, one of the sum.
@@ -152,6 +152,58 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t x, int lane) {
   x = __builtin_amdgcn_perm(y, x, lane & 1 ? 0x03070105u : 0x06020400u);
   y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true);                // lane ^ 2
   return __builtin_amdgcn_perm(y, x, lane & 2 ? 0x03020706u : 0x05040100u);
+}
+
+// ---------------------------------------------------------------------------
+// Norms: each element of a head times 1 / sqrt(mean square + eps) times its
+// weight.  A head lies in 2^ush neighbouring lanes of 16 elements each, or, where
+// a wave takes one token, in all its lanes.
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL> __device__ __forceinline__ double dpp(double v) {
+  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true),
+                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, true));
+}
+template <typename W>
+__device__ __forceinline__ W head_sum(W v, int ush) {
+  v += dpp<0xB1>(v);                                           // lane ^ 1
+  v += dpp<0x4E>(v);                                           // lane ^ 2
+  if (ush > 2) v += dpp<0x141>(v);                             // 7 - lane: the other four
+  if (ush > 3) v += dpp<0x140>(v);                             // 15 - lane: the other eight
+  return v;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v = head_sum(v, 4);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ double root(double sum, const KvAppend& A) { return rsqrt(sum / A.kv.dim + (double)A.eps); }
+__device__ __forceinline__ float root(float sum, const KvAppend& A) {
+  return 1.f / sqrtf(sum / (float)A.kv.dim + A.eps);
+}
+template <typename T>
+__device__ __forceinline__ const T* weights_of(const void* w, int32_t stride, int head) {
+  return (const T*)w + (int64_t)head * stride;
+}
+template <typename T>
+__device__ __forceinline__ Pairs<T> load_weights(const KvAppend& A, const void* w, int head, int a, int b) {
+  if (w) return load_pairs(A.kv, weights_of<T>(w, A.w_stride, head), a, b);
+  Pairs<T> r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.a[j] = r.b[j] = (T)1.f;
+  return r;
+}
+// q's norm: in fp32, whose squares and sums hold those of fp16 numbers; fp32 ones
+// may lie anywhere and take 64 bits.
+template <typename T> struct Norm { typedef float type; };
+template <> struct Norm<float> { typedef double type; };
+template <typename W, typename T>
+__device__ __forceinline__ W square_sum(const Pairs<T>& x) {
+  W s = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s += (W)x.a[j] * (W)x.a[j] + (W)x.b[j] * (W)x.b[j];
+  return s;
 }
 
 // ---------------------------------------------------------------------------
@@ -229,7 +281,7 @@ __device__ __forceinline__ Item item_of(const KvAppend& A, uint32_t at) {
 
 // One token of one head by a wave: lane v takes pair v of the keys and, of the
 // values, elements 2v and 2v + 1, which are two bytes of one 16-byte unit.
-template <typename T, int CODE>
+template <typename T, int CODE, bool NORM>
 __device__ __forceinline__ void store_one(const KvAppend& A, uint32_t at, int lane) {
   using C = Code<CODE>;
   constexpr int N = 2;                                         // pairs a lane: 1 up to 128 elements, 2 for 256
@@ -248,6 +300,17 @@ __device__ __forceinline__ void store_one(const KvAppend& A, uint32_t at, int la
   uint4 old[N];
   int da[N], db[N];
   uint32_t mk = 0, mv = 0;
+  double inv_rms = 1.;
+  if (NORM) {
+    double sum = 0.;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (2 * (lane + 64 * n) < dim) {
+        const double a = (double)kin[2 * (lane + 64 * n)], b = (double)kin[2 * (lane + 64 * n) + 1];
+        sum += a * a + b * b;
+      }
+    inv_rms = root(wave_sum(sum), A);
+  }
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int p = lane + 64 * n;
@@ -255,7 +318,17 @@ __device__ __forceinline__ void store_one(const KvAppend& A, uint32_t at, int la
     const bool turns = p < half, split = turns && kv.pairs == SLORA_KV_HALVES;
     da[n] = split ? p : 2 * p;
     db[n] = split ? half + p : 2 * p + 1;
-    turned((float)kin[da[n]], (float)kin[db[n]], turns ? cs[p] : 1.f, turns ? cs[half + p] : 0.f, &ka[n], &kb[n]);
+    double xa = (double)kin[da[n]], xb = (double)kin[db[n]];
+    if (NORM) {
+      const T* w = weights_of<T>(A.k_weight, A.w_stride, it.head);
+      xa *= inv_rms;
+      xb *= inv_rms;
+      if (A.k_weight) {
+        xa *= (double)w[da[n]];
+        xb *= (double)w[db[n]];
+      }
+    }
+    turned(xa, xb, turns ? cs[p] : 1.f, turns ? cs[half + p] : 0.f, &ka[n], &kb[n]);
     v0[n] = (float)vin[2 * p];
     v1[n] = (float)vin[2 * p + 1];
     // the unit's other tokens, of which none is there yet in the first one's case
@@ -303,7 +376,7 @@ __device__ __forceinline__ void store_one(const KvAppend& A, uint32_t at, int la
     }
 }
 
-template <typename T, int CODE>
+template <typename T, int CODE, bool NORM>
 __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int tid, uint32_t* lds) {
   using C = Code<CODE>;
   const KvView& kv = A.kv;
@@ -313,6 +386,13 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
   const T* in = (const T*)A.k + (int64_t)it.head * it.dim;
   const uint32_t held = blk.slot0 ? __float_as_uint(it.range[0]) & 0x7FFFFFFFu : 0;
 
+  // a thread's units are the same part of a head, token after token
+  Pairs<T> w;
+  if (NORM) {
+    int a, b;
+    unit_runs(kv, tid & ((1 << ush) - 1), &a, &b);
+    w = load_weights<T>(A, A.k_weight, it.head, a, b);
+  }
   auto load = [&](int u, Pairs<T>* x, Turn* t) {
     const int slot = blk.slot0 + (u >> ush), c = u & ((1 << ush) - 1);
     int a, b;
@@ -320,12 +400,18 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
     *x = load_pairs(kv, in + (it.row0 + slot) * A.k_stride, a, b);
     *t = load_turn(kv, A.cos_sin, it.pos0 + slot, c);
   };
-  auto largest = [&](const Pairs<T>& x, const Turn& t) {
+  // (a head's lanes are in a loop together: units are whole heads)
+  auto rms = [&](const Pairs<T>& x) { return NORM ? root(head_sum(square_sum<double>(x), ush), A) : 1.; };
+  auto turn = [&](const Pairs<T>& x, const Turn& t, double r, int j, double* ra, double* rb) {
+    if (NORM) turned((double)x.a[j] * r * (double)w.a[j], (double)x.b[j] * r * (double)w.b[j], t.c[j], t.s[j], ra, rb);
+    else turned((double)x.a[j], (double)x.b[j], t.c[j], t.s[j], ra, rb);
+  };
+  auto largest = [&](const Pairs<T>& x, const Turn& t, double r) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       double ra, rb;
-      turned((float)x.a[j], (float)x.b[j], t.c[j], t.s[j], &ra, &rb);
+      turn(x, t, r, j, &ra, &rb);
       m = max(m, max(magnitude(ra), magnitude(rb)));
     }
     return m;
@@ -333,19 +419,20 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
   Pairs<T> kept{};
   Turn kept_turn{};
   if (tid < units) load(tid, &kept, &kept_turn);
-  uint32_t m = largest(kept, kept_turn);
+  const double kept_rms = rms(kept);
+  uint32_t m = tid < units || !NORM ? largest(kept, kept_turn, kept_rms) : 0;
   for (int u = tid + kThreads; u < units; u += kThreads) {
     Pairs<T> x;
     Turn t;
     load(u, &x, &t);
-    m = max(m, largest(x, t));
+    m = max(m, largest(x, t, rms(x)));
   }
   m = max(team_max(m, lds), held);
   const bool bad = m >= 0x7F800000u;
   if (tid == 0) it.range[0] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m);
   const double grown = __uint_as_float(m), inv = m ? (double)C::kTop / grown : 0.;
 
-  auto put = [&](int u, const Pairs<T>& x, const Turn& t) {
+  auto put = [&](int u, const Pairs<T>& x, const Turn& t, double r) {
     const int slot = blk.slot0 + (u >> ush), c = u & ((1 << ush) - 1);
     int a, b;
     unit_runs(kv, c, &a, &b);
@@ -353,7 +440,7 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       double ra, rb;
-      turned((float)x.a[j], (float)x.b[j], t.c[j], t.s[j], &ra, &rb);
+      turn(x, t, r, j, &ra, &rb);
       wa[j >> 2] |= C::nearest(ra * inv) << (8 * (j & 3));
       wb[j >> 2] |= C::nearest(rb * inv) << (8 * (j & 3));
     }
@@ -368,12 +455,12 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
     *reinterpret_cast<uint2*>(it.page + kv_k_byte(slot, a, it.dim)) = first;
     *reinterpret_cast<uint2*>(it.page + kv_k_byte(slot, b, it.dim)) = second;
   };
-  if (tid < units) put(tid, kept, kept_turn);
+  if (tid < units) put(tid, kept, kept_turn, kept_rms);
   for (int u = tid + kThreads; u < units; u += kThreads) {
     Pairs<T> x;
     Turn t;
     load(u, &x, &t);
-    put(u, x, t);
+    put(u, x, t, rms(x));
   }
   if (blk.slot0 && m != held) {                                // the range grew: older keys are coded again
     const double ratio = bad ? 0. : (double)__uint_as_float(held) / grown;
@@ -475,7 +562,7 @@ __device__ __forceinline__ void store_values(const KvAppend& A, uint32_t at, int
 // blocks; and q, whose workgroups stream and are spread evenly among those,
 // which wait: a thread rotates one unit of A.q_heads heads of a row, so that a
 // row's angles are read once for them.
-template <typename T, int CODE>
+template <typename T, int CODE, bool NORM>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
   typedef typename Vec<T>::v8 V8;
   const KvView& kv = A.kv;
@@ -488,11 +575,11 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
     const uint32_t wg = blockIdx.x - q_wg, small = (uint32_t)A.n_small * kv.n_kv, small_wgs = (small + 3) / 4;
     if (wg < small_wgs) {
       const uint32_t item = uni(wg * 4 + (tid >> 6));
-      if (item < small) store_one<T, CODE>(A, item, tid & 63);
+      if (item < small) store_one<T, CODE, NORM>(A, item, tid & 63);
     } else {
       const uint32_t item = wg - small_wgs;
       if (item & 1) store_values<T, CODE>(A, small + (item >> 1), tid, lds);
-      else store_keys<T, CODE>(A, small + (item >> 1), tid, lds);
+      else store_keys<T, CODE, NORM>(A, small + (item >> 1), tid, lds);
     }
     return;
   }
@@ -509,14 +596,27 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
   const T* in = (const T*)A.q + row * A.q_stride;
   T* out = (T*)A.q_out + row * A.q_out_stride;
   const int h1 = min(kv.n_heads, h0 + A.q_heads);
-#pragma unroll 4
+  typedef typename Norm<T>::type W;
+  constexpr int kHeads = NORM ? 1 : 4;
+  Pairs<T> w;
+  if (NORM && !A.w_stride) w = load_weights<T>(A, A.q_weight, 0, a, b);
+#pragma unroll kHeads
   for (int h = h0; h < h1; ++h) {
     Pairs<T> x = load_pairs(kv, in + h * kv.dim, a, b);
-    if (turns) {
+    W r = 1;
+    if (NORM) {
+      if (A.w_stride) w = load_weights<T>(A, A.q_weight, h, a, b);
+      r = root(head_sum(square_sum<W>(x), ush), A);
+    }
+    if (NORM || turns) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float ra, rb;
-        turned((float)x.a[j], (float)x.b[j], t.c[j], t.s[j], &ra, &rb);
+        float xa = (float)x.a[j], xb = (float)x.b[j], ra, rb;
+        if (NORM) {
+          ra = xa = (float)((W)x.a[j] * r * (W)w.a[j]);
+          rb = xb = (float)((W)x.b[j] * r * (W)w.b[j]);
+        }
+        if (!NORM || turns) turned(xa, xb, t.c[j], t.s[j], &ra, &rb);
         x.a[j] = (T)ra;
         x.b[j] = (T)rb;
       }
@@ -1310,10 +1410,14 @@ hipError_t launch_kv_patch(int32_t* table, const KvPatch* patches, int32_t n, hi
                          args, 0, stream);
 }
 
-template <typename T>
+template <typename T, bool NORM>
 static const void* append_of(int code) {
-  return code == SLORA_KV_INT8 ? (const void*)kv_append_kernel<T, SLORA_KV_INT8>
-                               : (const void*)kv_append_kernel<T, SLORA_KV_FP8>;
+  return code == SLORA_KV_INT8 ? (const void*)kv_append_kernel<T, SLORA_KV_INT8, NORM>
+                               : (const void*)kv_append_kernel<T, SLORA_KV_FP8, NORM>;
+}
+template <bool NORM>
+static const void* append_of(int dtype, int code) {
+  return dtype == SLORA_F16 ? append_of<_Float16, NORM>(code) : append_of<float, NORM>(code);
 }
 template <typename T>
 static const void* read_of(int code) {
@@ -1342,7 +1446,7 @@ static const void* combine_of(int dim) {
          : dim == 128 ? (const void*)kv_combine_kernel<128> : (const void*)kv_combine_kernel<256>;
 }
 
-hipError_t launch_kv_append(const KvAppend& A0, hipStream_t stream) {
+hipError_t launch_kv_append(const KvAppend& A0, bool norm, hipStream_t stream) {
   KvAppend A = A0;
   const int64_t items = ((int64_t)A.n_small * A.kv.n_kv + 3) / 4 + 2 * (int64_t)(A.n_blocks - A.n_small) * A.kv.n_kv;
   int64_t q = 0;
@@ -1353,7 +1457,7 @@ hipError_t launch_kv_append(const KvAppend& A0, hipStream_t stream) {
   // workgroup b has q workgroups floor(b * share / 2^32) before it: with the
   // share rounded up, exactly q of all (there is always an item: q < all)
   A.q_share = (uint32_t)((((uint64_t)q << 32) + (uint64_t)(q + items) - 1) / (uint64_t)(q + items));
-  return run(A.kv.dtype == SLORA_F16 ? append_of<_Float16>(A.kv.code) : append_of<float>(A.kv.code), q + items, A,
+  return run(norm ? append_of<true>(A.kv.dtype, A.kv.code) : append_of<false>(A.kv.dtype, A.kv.code), q + items, A,
              stream);
 }
 

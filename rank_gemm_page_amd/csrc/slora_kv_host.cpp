@@ -272,6 +272,65 @@ slora_status launched(const std::string& f, hipError_t e) {
   return fail(SLORA_E_HIP, f + " launch: " + hipGetErrorString(e));
 }
 
+// An append, with the norms of q and k where norm is given.
+slora_status append(const std::string& f, slora_kv* kv, const slora_kv_step* st, int32_t layer, const void* q,
+                    int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, const slora_kv_norm* norm, const float* cos_sin, int64_t n_positions,
+                    void* stream) {
+  slora_status ok = check_launch(f, kv, st, layer);
+  if (ok != SLORA_OK) return ok;
+  if (st->reread) return fail(SLORA_E_INVAL, f + ": a reread step has no new tokens");
+  if (st->n_rows == 0) return SLORA_OK;
+  if (!k || !v) return fail(SLORA_E_INVAL, f + ": NULL k or v");
+  if (!q != !q_out) return fail(SLORA_E_INVAL, f + ": q and q_out must be given together");
+  if ((ok = check_rows(f, "k", kv, k, k_stride, kv->d.n_kv_heads)) != SLORA_OK) return ok;
+  if ((ok = check_rows(f, "v", kv, v, v_stride, kv->d.n_kv_heads)) != SLORA_OK) return ok;
+  if (q) {
+    if ((ok = check_rows(f, "q", kv, q, q_stride, kv->d.n_heads)) != SLORA_OK) return ok;
+    if ((ok = check_rows(f, "q_out", kv, q_out, q_out_stride, kv->d.n_heads)) != SLORA_OK) return ok;
+    if (q == q_out && q_stride != q_out_stride) return fail(SLORA_E_INVAL, f + ": q_out is q with another stride");
+  }
+  if (kv->d.rot_dim) {
+    if (!cos_sin || reinterpret_cast<uintptr_t>(cos_sin) & 15)
+      return fail(SLORA_E_INVAL, f + ": cos_sin must be non-NULL and 16-byte aligned");
+    if (n_positions < st->n_positions)
+      return fail(SLORA_E_INVAL, f + ": cos_sin does not hold every position of the step");
+  }
+  if ((ok = check_order(f, kv, st, layer)) != SLORA_OK) return ok;
+  if (!st->dev) return fail(SLORA_E_INVAL, f + ": step not uploaded (call slora_kv_step_upload)");
+  if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
+  KvAppend A{};
+  A.kv = kv->view();
+  A.blocks = reinterpret_cast<const KvBlock*>(st->dev);
+  A.n_blocks = (int32_t)st->blocks.size();
+  A.n_small = st->n_small;
+  A.n_rows = st->n_rows;
+  // enough threads for about eight waves a SIMD; beyond that, more heads a thread
+  const int64_t units = (int64_t)st->n_rows * kv->d.n_heads * kv->d.head_dim / 16;
+  A.q_heads = (int32_t)std::min<int64_t>(8, std::max<int64_t>(1, units / (1 << 19)));
+  A.layer = layer;
+  A.q = q;
+  A.q_out = q_out;
+  A.k = k;
+  A.v = v;
+  A.q_stride = q_stride;
+  A.q_out_stride = q_out_stride;
+  A.k_stride = k_stride;
+  A.v_stride = v_stride;
+  A.cos_sin = cos_sin;
+  A.row_pos = reinterpret_cast<const int32_t*>(st->dev + st->row_pos_off());
+  if (norm) {
+    A.q_weight = norm->q_weight;
+    A.k_weight = norm->k_weight;
+    A.eps = norm->eps;
+    A.w_stride = norm->per_head ? kv->d.head_dim : 0;
+  }
+  ok = launched(f, launch_kv_append(A, norm != nullptr, static_cast<hipStream_t>(stream)));
+  if (ok == SLORA_OK)
+    for (const KvBlock& b : st->blocks) kv->seqs[b.seq].stored[(size_t)b.block * kv->d.n_layers + layer] = b.slot1;
+  return ok;
+}
+
 }  // namespace
 
 extern "C" {
@@ -521,53 +580,81 @@ slora_status slora_kv_step_upload(slora_kv_step* st, void* dev_meta, size_t dev_
 slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* st, int32_t layer, const void* q, int64_t q_stride,
                              void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, const float* cos_sin, int64_t n_positions, void* stream) {
-  const std::string f = "slora_kv_append";
-  slora_status ok = check_launch(f, kv, st, layer);
+  return append("slora_kv_append", kv, st, layer, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, nullptr,
+                cos_sin, n_positions, stream);
+}
+
+slora_status slora_kv_append_norm(slora_kv* kv, const slora_kv_step* st, int32_t layer, const void* q, int64_t q_stride,
+                                  void* q_out, int64_t q_out_stride, const void* k, int64_t k_stride, const void* v,
+                                  int64_t v_stride, const slora_kv_norm* norm, const float* cos_sin,
+                                  int64_t n_positions, void* stream) {
+  const std::string f = "slora_kv_append_norm";
+  if (!norm) return fail(SLORA_E_INVAL, f + ": NULL norm");
+  if (!(norm->eps >= 0x1p-126f) || !std::isfinite(norm->eps))
+    return fail(SLORA_E_INVAL, f + ": eps must be at least 2^-126 and finite");
+  if (norm->per_head != 0 && norm->per_head != 1) return fail(SLORA_E_INVAL, f + ": per_head must be 0 or 1");
+  if ((reinterpret_cast<uintptr_t>(norm->q_weight) | reinterpret_cast<uintptr_t>(norm->k_weight)) & 15)
+    return fail(SLORA_E_INVAL, f + ": the weights must be 16-byte aligned");
+  return append(f, kv, st, layer, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, norm, cos_sin, n_positions,
+                stream);
+}
+
+// Frequencies are found in more than 64 bits, as turns a position.
+slora_status slora_kv_rotary_table(slora_kv* kv, const slora_kv_rotary* r, int64_t first, int64_t n, float* cos_sin,
+                                   void* stream) {
+  const std::string f = "slora_kv_rotary_table";
+  if (!kv || !r || !cos_sin) return fail(SLORA_E_INVAL, f + ": NULL argument");
+  const int32_t rot = kv->d.rot_dim;
+  if (!rot) return fail(SLORA_E_INVAL, f + ": the cache rotates nothing (rot_dim 0)");
+  if (reinterpret_cast<uintptr_t>(cos_sin) & 15) return fail(SLORA_E_INVAL, f + ": cos_sin must be 16-byte aligned");
+  constexpr int64_t kMostPositions = (int64_t)1 << 30;
+  if (first < 0 || n < 0 || first > kMostPositions || n > kMostPositions - first)
+    return fail(SLORA_E_INVAL, f + ": positions must be 0 .. 2^30");
+  if (r->reserved0 != 0) return fail(SLORA_E_INVAL, f + ": reserved0 must be 0");
+  if (r->scaling < SLORA_KV_ROT_NONE || r->scaling > SLORA_KV_ROT_RAMP)
+    return fail(SLORA_E_INVAL, f + ": unknown scaling");
+  if (!(r->base > 1.) || !std::isfinite(r->base)) return fail(SLORA_E_INVAL, f + ": base must be above 1 and finite");
+  if (!std::isfinite(r->amplitude)) return fail(SLORA_E_INVAL, f + ": amplitude must be finite");
+  const bool scaled = r->scaling != SLORA_KV_ROT_NONE;
+  if (scaled && (!(r->factor >= 1.) || !std::isfinite(r->factor)))
+    return fail(SLORA_E_INVAL, f + ": factor must be at least 1 and finite");
+  if (r->scaling == SLORA_KV_ROT_BANDS || r->scaling == SLORA_KV_ROT_RAMP) {
+    if (!(r->trained >= 1.) || !std::isfinite(r->trained))
+      return fail(SLORA_E_INVAL, f + ": trained must be at least 1 and finite");
+    if (!(r->low > 0.) || !(r->high > r->low) || !std::isfinite(r->high))
+      return fail(SLORA_E_INVAL, f + ": low and high must be finite, 0 < low < high");
+  }
+  if (n == 0) return SLORA_OK;
+  typedef long double wide;
+  const wide pi2 = 6.283185307179586476925286766559005768L, factor = scaled ? (wide)r->factor : 1.L;
+  wide log_base = std::log((wide)r->base);
+  if (r->scaling == SLORA_KV_ROT_BASE) log_base += std::log(factor) * rot / (rot - 2);
+  auto pair_of = [&](double turns) { return rot * std::log((wide)r->trained / (pi2 * turns)) / (2 * log_base); };
+  KvRotary R{};
+  for (int32_t i = 0; i < rot / 2; ++i) {
+    wide t = std::exp(-2 * i * log_base / rot), keep = 1.L;
+    if (r->scaling == SLORA_KV_ROT_LINEAR) keep = 0.L;
+    if (r->scaling == SLORA_KV_ROT_BANDS)
+      keep = (r->trained * t / pi2 - r->low) / ((wide)r->high - r->low);
+    if (r->scaling == SLORA_KV_ROT_RAMP) {
+      const wide high = std::max(std::floor(pair_of(r->high)), 0.L);
+      const wide low = std::min(std::ceil(pair_of(r->low)), (wide)(rot - 1));
+      keep = 1.L - (i - high) / std::max(low - high, 0.001L);
+    }
+    keep = std::min(std::max(keep, 0.L), 1.L);
+    if (keep < 1.L) t *= keep + (1.L - keep) / factor;
+    t /= pi2;
+    R.turn_hi[i] = (double)t;
+    R.turn_lo[i] = (double)(t - (wide)R.turn_hi[i]);
+  }
+  R.amplitude = r->amplitude;
+  R.out = cos_sin;
+  R.first = first;
+  R.n = n;
+  R.half = rot / 2;
+  slora_status ok = pool_device_current(kv->pool);
   if (ok != SLORA_OK) return ok;
-  if (st->reread) return fail(SLORA_E_INVAL, f + ": a reread step has no new tokens");
-  if (st->n_rows == 0) return SLORA_OK;
-  if (!k || !v) return fail(SLORA_E_INVAL, f + ": NULL k or v");
-  if (!q != !q_out) return fail(SLORA_E_INVAL, f + ": q and q_out must be given together");
-  if ((ok = check_rows(f, "k", kv, k, k_stride, kv->d.n_kv_heads)) != SLORA_OK) return ok;
-  if ((ok = check_rows(f, "v", kv, v, v_stride, kv->d.n_kv_heads)) != SLORA_OK) return ok;
-  if (q) {
-    if ((ok = check_rows(f, "q", kv, q, q_stride, kv->d.n_heads)) != SLORA_OK) return ok;
-    if ((ok = check_rows(f, "q_out", kv, q_out, q_out_stride, kv->d.n_heads)) != SLORA_OK) return ok;
-    if (q == q_out && q_stride != q_out_stride) return fail(SLORA_E_INVAL, f + ": q_out is q with another stride");
-  }
-  if (kv->d.rot_dim) {
-    if (!cos_sin || reinterpret_cast<uintptr_t>(cos_sin) & 15)
-      return fail(SLORA_E_INVAL, f + ": cos_sin must be non-NULL and 16-byte aligned");
-    if (n_positions < st->n_positions)
-      return fail(SLORA_E_INVAL, f + ": cos_sin does not hold every position of the step");
-  }
-  if ((ok = check_order(f, kv, st, layer)) != SLORA_OK) return ok;
-  if (!st->dev) return fail(SLORA_E_INVAL, f + ": step not uploaded (call slora_kv_step_upload)");
-  if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
-  KvAppend A{};
-  A.kv = kv->view();
-  A.blocks = reinterpret_cast<const KvBlock*>(st->dev);
-  A.n_blocks = (int32_t)st->blocks.size();
-  A.n_small = st->n_small;
-  A.n_rows = st->n_rows;
-  // enough threads for about eight waves a SIMD; beyond that, more heads a thread
-  const int64_t units = (int64_t)st->n_rows * kv->d.n_heads * kv->d.head_dim / 16;
-  A.q_heads = (int32_t)std::min<int64_t>(8, std::max<int64_t>(1, units / (1 << 19)));
-  A.layer = layer;
-  A.q = q;
-  A.q_out = q_out;
-  A.k = k;
-  A.v = v;
-  A.q_stride = q_stride;
-  A.q_out_stride = q_out_stride;
-  A.k_stride = k_stride;
-  A.v_stride = v_stride;
-  A.cos_sin = cos_sin;
-  A.row_pos = reinterpret_cast<const int32_t*>(st->dev + st->row_pos_off());
-  ok = launched(f, launch_kv_append(A, static_cast<hipStream_t>(stream)));
-  if (ok == SLORA_OK)
-    for (const KvBlock& b : st->blocks) kv->seqs[b.seq].stored[(size_t)b.block * kv->d.n_layers + layer] = b.slot1;
-  return ok;
+  return launched(f, launch_kv_rotary(R, static_cast<hipStream_t>(stream)));
 }
 
 slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* st, int32_t layer, const void* q, int64_t q_stride,

@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import numpy as np
 
@@ -30,6 +30,9 @@ SLORA_TUNE_FWD_GROUP, SLORA_TUNE_FWD_TILE, SLORA_TUNE_SHRINK_ROWS, SLORA_TUNE_FW
 
 SLORA_KV_INT8, SLORA_KV_FP8 = 0, 1
 SLORA_KV_HALVES, SLORA_KV_NEIGHBOURS = 0, 1
+SLORA_KV_ROT_NONE, SLORA_KV_ROT_LINEAR, SLORA_KV_ROT_BASE, SLORA_KV_ROT_BANDS, SLORA_KV_ROT_RAMP = 0, 1, 2, 3, 4
+_ROT_SCALINGS = {"none": SLORA_KV_ROT_NONE, "linear": SLORA_KV_ROT_LINEAR, "base": SLORA_KV_ROT_BASE,
+                 "bands": SLORA_KV_ROT_BANDS, "ramp": SLORA_KV_ROT_RAMP}
 
 EXPORTED = [
     "slora_pool_create", "slora_pool_destroy", "slora_pool_set_tuning", "slora_alloc_pages",
@@ -45,6 +48,7 @@ EXPORTED = [
     "slora_kv_device_bytes", "slora_kv_create", "slora_kv_destroy", "slora_kv_drop", "slora_kv_length",
     "slora_kv_pages", "slora_kv_build_step", "slora_kv_step_destroy", "slora_kv_step_get_info",
     "slora_kv_step_upload", "slora_kv_append", "slora_kv_attend", "slora_kv_read",
+    "slora_kv_append_norm", "slora_kv_rotary_table",
 ]
 # include/slora_probe.h: bandwidth probes (measurement only)
 EXPORTED_PROBE = ["slora_probe_read", "slora_probe_gather"]
@@ -81,6 +85,16 @@ class KvStepInfo(ctypes.Structure):
     _fields_ = [(name, c_int32) for name in
                 ("n_seqs", "n_rows", "max_len", "n_blocks", "n_new_pages", "n_row_tiles", "n_prompt_tiles",
                  "reserved0")] + [("meta_bytes", c_size_t), ("workspace_bytes", c_size_t)]
+
+
+class KvNorm(ctypes.Structure):
+    _fields_ = [("q_weight", c_void_p), ("k_weight", c_void_p), ("eps", c_float), ("per_head", c_int32)]
+
+
+class KvRotary(ctypes.Structure):
+    _fields_ = [("scaling", c_int32), ("reserved0", c_int32)] + [(name, c_double) for name in
+                                                                 ("base", "factor", "trained", "low", "high",
+                                                                  "amplitude")]
 
 
 class Pool(c_void_p):
@@ -164,6 +178,9 @@ def lib():
             "slora_kv_step_upload": (c_int32, [P, P, c_size_t, P]),
             "slora_kv_append": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, P, c_int64, P, c_int64, P, c_int64,
                                           P]),
+            "slora_kv_append_norm": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, P, c_int64, P, c_int64,
+                                               POINTER(KvNorm), P, c_int64, P]),
+            "slora_kv_rotary_table": (c_int32, [P, POINTER(KvRotary), c_int64, c_int64, P, P]),
             "slora_kv_attend": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, c_float, c_int32, P, c_size_t, P]),
             "slora_kv_read": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, P]),
             "slora_probe_read": (c_int32, [P, c_int64, c_int32, c_int32, P, P, P, P]),
@@ -659,6 +676,51 @@ def slora_kv_append(kv, step, layer: int, k, v, q=None, q_out=None, cos_sin=None
     status = kv.api.slora_kv_append(kv, step, layer, qp, qs, op, os_, kp, ks, vp, vs, cs, n_positions, _stream(stream))
     if status:
         _check(status, "slora_kv_append")
+
+
+def _weight(x, kv, heads: int, per_head: bool, what: str) -> int:
+    """Address of a norm's weights: a contiguous tensor of the pool's type on its GPU, [head_dim] or, with per_head,
+    [heads, head_dim], a raw address, or None (ones)."""
+    if not hasattr(x, "get_device"):
+        return _ptr(x)
+    dim = kv.desc.head_dim
+    shape = (heads, dim) if per_head else (dim,)
+    if tuple(x.shape) != shape or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {list(shape)} tensor, got {tuple(x.shape)}")
+    if kv.dtype is not None and _type_name(x.dtype) != kv.dtype:
+        raise ValueError(f"expected the pool's type, {kv.dtype}, got {x.dtype}")
+    if x.get_device() != kv.device:
+        _on_device(x, kv.device, what)
+    return x.data_ptr()
+
+
+def slora_kv_append_norm(kv, step, layer: int, k, v, q=None, q_out=None, q_weight=None, k_weight=None,
+                         eps: float = 1e-6, per_head: bool = False, cos_sin=None, stream=None, k_stride=None,
+                         v_stride=None, q_stride=None, q_out_stride=None, n_positions=None) -> None:
+    """slora_kv_append with q and k normed head by head first; weights of all heads [head_dim], or [heads, head_dim]."""
+    heads, kv_heads = kv.heads
+    cs, n_positions = _angles(cos_sin, n_positions, kv)
+    qp, qs = _rows(q, step, heads, q_stride)
+    op, os_ = _rows(q_out, step, heads, q_out_stride)
+    kp, ks = _rows(k, step, kv_heads, k_stride)
+    vp, vs = _rows(v, step, kv_heads, v_stride)
+    norm = KvNorm(_weight(q_weight, kv, heads, per_head, "q_weight"),
+                  _weight(k_weight, kv, kv_heads, per_head, "k_weight"), eps, int(per_head))
+    status = kv.api.slora_kv_append_norm(kv, step, layer, qp, qs, op, os_, kp, ks, vp, vs, ctypes.byref(norm), cs,
+                                         n_positions, _stream(stream))
+    if status:
+        _check(status, "slora_kv_append_norm")
+
+
+def slora_kv_rotary_table(kv, cos_sin, first: int = 0, base: float = 10000.0, scaling="none", factor: float = 1.0,
+                          trained: float = 0.0, low: float = 0.0, high: float = 0.0, amplitude: float = 1.0,
+                          stream=None, n_positions=None) -> None:
+    """Positions first, first + 1, ... into cos_sin, a contiguous fp32 tensor [n_positions, rot_dim] (or a raw address
+    with n_positions).  scaling: "none", "linear", "base", "bands" or "ramp", or its SLORA_KV_ROT_ number."""
+    table, n_positions = _angles(cos_sin, n_positions, kv)
+    desc = KvRotary(_ROT_SCALINGS.get(scaling, scaling), 0, base, factor, trained, low, high, amplitude)
+    _check(kv.api.slora_kv_rotary_table(kv, ctypes.byref(desc), first, n_positions, table, _stream(stream)),
+           "slora_kv_rotary_table")
 
 
 def slora_kv_attend(kv, step, layer: int, q, out, scale: float, window: int = 0, workspace=None,
