@@ -585,6 +585,14 @@ slora_status slora_kv_pages(const slora_kv* kv, int32_t seq, int32_t layer, int3
  * rows whose keys and values are stored already.  Host only. */
 slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, const int32_t* counts,
                                  int32_t reread, slora_kv_step** out);
+/* The same for layers whose attention sees a window of tokens and the first
+ * `sinks` ones (slora_kv_attend_sinks): the work of attention launches is cut for
+ * what the rows see then.  It changes how the work is cut, never what is
+ * computed: such a step takes launches of any window, and any step takes launches
+ * of this one.  A model with layers of both kinds runs the others on a reread step
+ * of the same rows.  window 0: none; sinks >= 0. */
+slora_status slora_kv_build_step_window(slora_kv* kv, int32_t n, const int32_t* seqs, const int32_t* counts,
+                                        int32_t reread, int32_t window, int32_t sinks, slora_kv_step** out);
 void slora_kv_step_destroy(slora_kv_step* step);
 
 typedef struct {
@@ -698,6 +706,14 @@ slora_status slora_kv_rotary_table(slora_kv* kv, const slora_kv_rotary* rotary, 
 slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* step, int32_t layer, const void* q,
                              int64_t q_stride, void* out, int64_t out_stride, float scale, int32_t window,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* slora_kv_attend where the first `sinks` (>= 0) tokens of a sequence stay visible
+ * beside the window: over positions j <= p with j > p - window or j < sinks
+ * (window 0: all).  A step cut for the window (slora_kv_build_step_window) spreads
+ * few rows over more of the chip. */
+slora_status slora_kv_attend_sinks(slora_kv* kv, const slora_kv_step* step, int32_t layer, const void* q,
+                                   int64_t q_stride, void* out, int64_t out_stride, float scale, int32_t window,
+                                   int32_t sinks, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Read the cached keys and values of the step's rows in `layer` back, as the
  * values their codes stand for (keys as they were stored: rotated), rounded

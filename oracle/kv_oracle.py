@@ -143,9 +143,9 @@ class KvModel:
         r = ranges[np.arange(first, last) // self.block][:, :, None]
         return codes[first:last] * r / TOP[self.code]
 
-    def attend(self, seq, layer, q, start, scale, window=0, length=None):
+    def attend(self, seq, layer, q, start, scale, window=0, length=None, sinks=0):
         """Rows q [n, n_heads, dim] (rotated) at positions start, start + 1, ... over the first `length` tokens (all by
-        default).  Returns the output and, per output, sum_j w_j |v_j|, the largest sum of |scale q k| over the seen
+        default), each over the window and the first `sinks` tokens.  Returns the output and, per output, sum_j w_j |v_j|, the largest sum of |scale q k| over the seen
         keys and sum_j |v_j| / sum_j exp(s_j - max s) for error bounds."""
         k, v = (self.values(seq, layer, w, 0, length) for w in (0, 1))
         q = np.asarray(q, np.float64)
@@ -155,7 +155,8 @@ class KvModel:
             p = start + t
             lo = max(0, p - window + 1) if window else 0
             for h in range(self.n_heads):
-                kk, vv = k[lo:p + 1, h // g], v[lo:p + 1, h // g]
+                seen = np.r_[0:min(sinks, lo), lo:p + 1]
+                kk, vv = k[seen, h // g], v[seen, h // g]
                 s = scale * (kk @ q[t, h])
                 with np.errstate(invalid="ignore"):
                     e = np.exp(s - s.max())

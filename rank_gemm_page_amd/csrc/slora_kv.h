@@ -72,7 +72,7 @@ struct KvAttend {
   const KvTile* tiles;        // row tiles
   const KvTile* combine;      // of split prompt tiles
   uint32_t* counters;         // of split row tiles: zero before and after every launch
-  int32_t n_prompts, n_tiles, n_combine, layer, window;
+  int32_t n_prompts, n_tiles, n_combine, layer, window, sinks;
   const void* q; void* out;
   int64_t q_stride, out_stride;
   float scale_log2;           // scale * log2(e)

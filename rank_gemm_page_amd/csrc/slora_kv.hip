@@ -719,12 +719,33 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, int splits, uint32_t*
   return *lds == (uint32_t)splits - 1;
 }
 
+// Groups of 32 keys that a tile sees, from key lo to key last: with sinks, the
+// groups of the first tokens and then the window's are counted as one run, of
+// which the first `sinks` lie at the sequence's start.
+template <bool SINKS> struct Seen;
+template <> struct Seen<false> {
+  static constexpr int sinks = 0;
+  int first, last;
+  __device__ Seen(const KvAttend&, int lo, int last_key) : first(lo / kKvGroup), last(last_key / kKvGroup + 1) {}
+  __device__ int group(int i) const { return i; }
+};
+template <> struct Seen<true> {
+  static constexpr int first = 0;
+  int last, sinks, skip;
+  __device__ Seen(const KvAttend& A, int lo, int last_key) {
+    sinks = min((A.sinks + kKvGroup - 1) / kKvGroup, lo / kKvGroup);
+    skip = lo / kKvGroup - sinks;
+    last = last_key / kKvGroup + 1 - skip;
+  }
+  __device__ int group(int i) const { return i < sinks ? i : i + skip; }
+};
+
 // The bound of two waves a SIMD makes the compiler spare registers: three run at
 // heads of 128 (147 registers instead of 184, decode batch 374 to 350 us) and five
 // at 64.  Heads of 256 reach two by loading the next keys only when these are
 // multiplied (f16 324 to 194 registers, 16 requests of 4500 to 9000 tokens, 16
 // heads on 4, 88 to 59 us).
-template <typename T, int CODE, int D>
+template <typename T, int CODE, int D, bool SINKS>
 __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A) {
   using F = typename Frag<T>::type;
   constexpr int NC = D / 64, NE = D / 32, NT = D / 16;
@@ -762,7 +783,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
   }
 
   // groups of 32 keys of this tile, of this split, of this wave
-  const int first = tile_lo / kKvGroup, last = pos_last / kKvGroup + 1;
+  const Seen<SINKS> seen_groups(A, tile_lo, pos_last);
+  const int first = seen_groups.first, last = seen_groups.last;
   const int per = (last - first + tile.splits - 1) / tile.splits;
   const int s_lo = first + tile.split * per, s_hi = min(last, s_lo + per);
   const int per_wave = (max(0, s_hi - s_lo) + 3) / 4;
@@ -777,7 +799,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
   float m = -FLT_MAX, l = 0.f, ref = 0.f;
 
   const bool once = packed <= kKvRows;
-  int b = gi / nb, sub = gi - b * nb;
+  int b = seen_groups.group(gi) / nb, sub = seen_groups.group(gi) - b * nb, next = gi;
   uint4 kf[2 * NC], vf[NE];
   float rk = 0.f, rv = 0.f;
   auto load = [&](uint4* kx, uint4* vx, float& xk, float& xv) {
@@ -800,13 +822,17 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
     xk = kv.range[2 * (int64_t)page];
     xv = kv.range[2 * (int64_t)page + 1];
     if (++sub == nb) { sub = 0; ++b; }
+    if (SINKS && ++next == seen_groups.sinks) {
+      b = seen_groups.group(next) / nb;
+      sub = seen_groups.group(next) - b * nb;
+    }
   };
   if (gi < ge) load(kf, vf, rk, rv);
   for (; gi < ge; ++gi) {
     uint4 kn[2 * NC], vn[NE];
     float rkn = 0.f, rvn = 0.f;
     if (D < 256 && gi + 1 < ge) load(kn, vn, rkn, rvn);
-    const int key0 = gi * kKvGroup;
+    const int key0 = seen_groups.group(gi) * kKvGroup;
 
     // (a NaN range holds zero codes: its keys must be NaN, its values stay 0 for the rows that do not see them)
     const float uk = values ? rk / Code<CODE>::kTop : 1.f, uv = values && rv > 0.f ? rv / Code<CODE>::kTop : 0.f;
@@ -830,12 +856,12 @@ __global__ __launch_bounds__(kThreads, 2) void kv_attend_rows_kernel(KvAttend A)
     // keys behind the sequence hold anything: their scores are replaced, and
     // their e4m3 bytes, which may be NaN, are cleared
     bool seen = true;
-    if (key0 + kKvGroup - 1 > pos_first || key0 < all_lo) {
+    if (key0 + kKvGroup - 1 > pos_first || (key0 < all_lo && !(SINKS && key0 + kKvGroup <= A.sinks))) {
       seen = false;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int key = key0 + (j >> 2) * 16 + g * 4 + (j & 3);
-        const bool in = key <= pos && key >= lo;
+        const bool in = key <= pos && (key >= lo || (SINKS && key < A.sinks));
         x[j] = in ? x[j] : -INFINITY;
         seen |= in;
       }
@@ -1015,7 +1041,7 @@ __device__ __forceinline__ int v_slot(int d, int t, int h) {
   return p * 8 + (((d & 1) * 4 + 2 * t + h) ^ ((p >> 1 & 1) | (p >> 2 & 2) | (p & 4)));
 }
 
-template <int CODE, int D, bool TRIPLE>
+template <int CODE, int D, bool TRIPLE, bool SINKS>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_attend_prompt_kernel(KvAttend A) {
   constexpr int NG = D == 256 || TRIPLE ? 1 : 2; // groups of 32 keys staged at a time
   constexpr int KS = D / 16, NB = D / 32;        // steps of the K product, blocks of 32 elements
@@ -1052,7 +1078,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
     }
   }
   const float scale = fabsf(A.scale_log2) / Code<CODE>::kTop;
-  const int g_lo = (A.window ? max(0, wg_first - A.window + 1) : 0) / kKvGroup, g_hi = wg_last / kKvGroup + 1;
+  const Seen<SINKS> seen_groups(A, A.window ? max(0, wg_first - A.window + 1) : 0, wg_last);
+  const int g_lo = seen_groups.first, g_hi = seen_groups.last;
   const int per = (g_hi - g_lo + tile.splits - 1) / tile.splits;
   const int g_begin = uni(g_lo + tile.split * per), g_end = uni(min(g_hi, g_begin + per));
   const int32_t* row = kv_row(kv, tile.seq, A.layer, head);
@@ -1064,7 +1091,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
   auto load = [&](int g) {
 #pragma unroll
     for (int x = 0; x < NG; ++x) {
-      const int gg = min(g + x, g_end - 1), b = gg / nb, sub = gg - b * nb;
+      const int gg = seen_groups.group(min(g + x, g_end - 1)), b = gg / nb, sub = gg - b * nb;
       const int32_t page = uni(row[b]);
       const char* kb = kv.base + (int64_t)page * kv.page_bytes + (int64_t)sub * kKvGroup * D;
       const char* vb = kb + (int64_t)kv.block * D;
@@ -1091,11 +1118,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
       const int vg = uu % 64 / 16, d = uu / 64 * 32 + uu % 16 * 2;
       uint4 c = vc[u];
       // e4m3 bytes behind the sequence may be NaN, which a weight of zero keeps
-      if (CODE == SLORA_KV_FP8 && (g + x) * kKvGroup + kKvGroup > len) {
+      const int key0 = seen_groups.group(g + x) * kKvGroup;
+      if (CODE == SLORA_KV_FP8 && key0 + kKvGroup > len) {
         uint32_t keep[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if ((g + x) * kKvGroup + (j >> 2) * 16 + vg * 4 + (j & 3) < len) keep[j >> 2] |= 0xFFu << (8 * (j & 3));
+          if (key0 + (j >> 2) * 16 + vg * 4 + (j & 3) < len) keep[j >> 2] |= 0xFFu << (8 * (j & 3));
         c = make_uint4(c.x & keep[0], c.y & keep[1], c.z & keep[0], c.w & keep[1]);
       }
       // lanes vg and vg + 2 (32 apart) hold the two quads of tokens of a slot: the
@@ -1127,8 +1155,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
     if (more) load(gb + NG);
 #pragma unroll
     for (int x = 0; x < NG; ++x) {
-      const int key0 = (gb + x) * kKvGroup;
-      if (gb + x >= g_end || key0 > w_last || key0 + kKvGroup <= w_lo || (TRIPLE && idle)) continue;
+      const int key0 = seen_groups.group(gb + x) * kKvGroup;
+      if (gb + x >= g_end || key0 > w_last || (key0 + kKvGroup <= w_lo && !(SINKS && key0 < A.sinks)) ||
+          (TRIPLE && idle))
+        continue;
       float16v s = {};
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -1139,12 +1169,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : TRIPLE ? 3 : 2) void kv_at
       float ck = rk[x] * scale;
       ck = ck > 0.f ? ck : FLT_MIN;
       bool seen = true;
-      if (key0 + kKvGroup - 1 > w_first || key0 < w_all) {
+      if (key0 + kKvGroup - 1 > w_first || (key0 < w_all && !(SINKS && key0 + kKvGroup <= A.sinks))) {
         seen = false;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int key = key0 + (j >> 2) * 8 + h * 4 + (j & 3);
-          const bool in = (uint32_t)(pos - key) < window;      // key <= pos and key > pos - window
+          bool in = (uint32_t)(pos - key) < window;            // key <= pos and key > pos - window
+          if (SINKS) in |= key < A.sinks && key <= pos;
           s[j] = in ? s[j] : -INFINITY;
           seen |= in;
         }
@@ -1424,22 +1455,31 @@ static const void* read_of(int code) {
   return code == SLORA_KV_INT8 ? (const void*)kv_read_kernel<T, SLORA_KV_INT8>
                                : (const void*)kv_read_kernel<T, SLORA_KV_FP8>;
 }
-template <typename T, int CODE>
+template <typename T, int CODE, bool SINKS>
 static const void* rows_of(int dim) {
-  return dim == 64 ? (const void*)kv_attend_rows_kernel<T, CODE, 64>
-         : dim == 128 ? (const void*)kv_attend_rows_kernel<T, CODE, 128>
-                      : (const void*)kv_attend_rows_kernel<T, CODE, 256>;
+  return dim == 64 ? (const void*)kv_attend_rows_kernel<T, CODE, 64, SINKS>
+         : dim == 128 ? (const void*)kv_attend_rows_kernel<T, CODE, 128, SINKS>
+                      : (const void*)kv_attend_rows_kernel<T, CODE, 256, SINKS>;
 }
-template <typename T>
+template <typename T, bool SINKS>
 static const void* rows_of(int code, int dim) {
-  return code == SLORA_KV_INT8 ? rows_of<T, SLORA_KV_INT8>(dim) : rows_of<T, SLORA_KV_FP8>(dim);
+  return code == SLORA_KV_INT8 ? rows_of<T, SLORA_KV_INT8, SINKS>(dim) : rows_of<T, SLORA_KV_FP8, SINKS>(dim);
 }
-template <int CODE>
+template <bool SINKS>
+static const void* rows_of(bool half, int code, int dim) {
+  return half ? rows_of<_Float16, SINKS>(code, dim) : rows_of<float, SINKS>(code, dim);
+}
+template <int CODE, bool SINKS>
 static const void* prompt_of(int dim, bool triple) {
-  return dim == 64 ? (const void*)kv_attend_prompt_kernel<CODE, 64, false>
-         : dim == 256 ? (const void*)kv_attend_prompt_kernel<CODE, 256, false>
-         : triple ? (const void*)kv_attend_prompt_kernel<CODE, 128, true>
-                  : (const void*)kv_attend_prompt_kernel<CODE, 128, false>;
+  return dim == 64 ? (const void*)kv_attend_prompt_kernel<CODE, 64, false, SINKS>
+         : dim == 256 ? (const void*)kv_attend_prompt_kernel<CODE, 256, false, SINKS>
+         : triple ? (const void*)kv_attend_prompt_kernel<CODE, 128, true, SINKS>
+                  : (const void*)kv_attend_prompt_kernel<CODE, 128, false, SINKS>;
+}
+template <bool SINKS>
+static const void* prompt_of(int code, int dim, bool triple) {
+  return code == SLORA_KV_INT8 ? prompt_of<SLORA_KV_INT8, SINKS>(dim, triple)
+                               : prompt_of<SLORA_KV_FP8, SINKS>(dim, triple);
 }
 static const void* combine_of(int dim) {
   return dim == 64 ? (const void*)kv_combine_kernel<64>
@@ -1474,12 +1514,12 @@ hipError_t launch_kv_attend(const KvAttend& A, hipStream_t stream) {
   // and 8 heads one prompt of 4096 (5 a CU): 239 | 247.
   const int64_t prompts = (int64_t)A.n_prompts * A.kv.n_kv;
   const bool triple = (prompts - 1) / (3 * kKvCus) < (prompts - 1) / (2 * kKvCus);
-  hipError_t e = run(A.kv.code == SLORA_KV_INT8 ? prompt_of<SLORA_KV_INT8>(A.kv.dim, triple)
-                                                : prompt_of<SLORA_KV_FP8>(A.kv.dim, triple),
+  hipError_t e = run(A.sinks ? prompt_of<true>(A.kv.code, A.kv.dim, triple)
+                             : prompt_of<false>(A.kv.code, A.kv.dim, triple),
                      prompts, A, stream);
   if (e != hipSuccess) return e;
-  e = run(half ? rows_of<_Float16>(A.kv.code, A.kv.dim) : rows_of<float>(A.kv.code, A.kv.dim),
-                     (int64_t)A.n_tiles * A.kv.n_kv, A, stream);
+  e = run(A.sinks ? rows_of<true>(half, A.kv.code, A.kv.dim) : rows_of<false>(half, A.kv.code, A.kv.dim),
+          (int64_t)A.n_tiles * A.kv.n_kv, A, stream);
   if (e != hipSuccess) return e;
   return run(combine_of(A.kv.dim), (int64_t)A.n_combine * A.kv.n_kv * kKvRows, A, stream);
 }

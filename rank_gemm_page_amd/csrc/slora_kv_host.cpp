@@ -161,15 +161,19 @@ constexpr int64_t kMinGroups = 8, kWantGroups = 1536;
 constexpr int64_t kPromptMin = 96, kFreshMin = 48, kPromptGroups = 16, kWantPrompts = 1024;
 
 // Tiles of 128 packed rows for long runs of rows (fp16), and row tiles of 16 for
-// the others, with their key splits, longest first.
-void build_tiles(slora_kv_step* st) {
+// the others, with their key splits, longest first.  Splits are cut for a window
+// (0: none) and the first `sinks` tokens.
+void build_tiles(slora_kv_step* st, int32_t window, int32_t sinks) {
   const slora_kv_desc& d = st->kv->d;
   const int32_t G = d.n_heads / d.n_kv_heads;
   const bool half = st->kv->info.dtype == SLORA_F16;
   auto prompt = [&](const StepSeq& s) { return half && (int64_t)s.rows * G >= (s.start ? kPromptMin : kFreshMin); };
-  // key groups that the tile of packed rows [r0, r0 + n) sees, without a window
+  // key groups that the tile of packed rows [r0, r0 + n) sees
   auto groups_of = [&](const StepSeq& s, int64_t r0, int64_t n) {
-    return (s.start + (std::min<int64_t>(r0 + n, (int64_t)s.rows * G) - 1) / G) / kKvGroup + 1;
+    const int64_t last = (s.start + (std::min<int64_t>(r0 + n, (int64_t)s.rows * G) - 1) / G) / kKvGroup + 1;
+    if (!window) return last;
+    const int64_t first = std::max<int64_t>(0, s.start + r0 / G - window + 1) / kKvGroup;
+    return last - first + std::min<int64_t>(((int64_t)sinks + kKvGroup - 1) / kKvGroup, first);
   };
   // groups of a workgroup: the fewest for which all row tiles' workgroups are at most kWantGroups
   std::vector<int64_t> lens;
@@ -331,6 +335,47 @@ slora_status append(const std::string& f, slora_kv* kv, const slora_kv_step* st,
   return ok;
 }
 
+slora_status attend(const std::string& f, slora_kv* kv, const slora_kv_step* st, int32_t layer, const void* q,
+                    int64_t q_stride, void* out, int64_t out_stride, float scale, int32_t window, int32_t sinks,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  slora_status ok = check_launch(f, kv, st, layer);
+  if (ok != SLORA_OK) return ok;
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return fail(SLORA_E_INVAL, f + ": scale times log2(e) must be finite in fp32");
+  if (window < 0) return fail(SLORA_E_INVAL, f + ": window must be 0 (none) or positive");
+  if (sinks < 0) return fail(SLORA_E_INVAL, f + ": sinks must be 0 or positive");
+  if (st->n_rows == 0) return SLORA_OK;
+  if (!q || !out) return fail(SLORA_E_INVAL, f + ": NULL q or out");
+  if ((ok = check_rows(f, "q", kv, q, q_stride, kv->d.n_heads)) != SLORA_OK) return ok;
+  if ((ok = check_rows(f, "out", kv, out, out_stride, kv->d.n_heads)) != SLORA_OK) return ok;
+  if (st->workspace() > 0) {
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) & 15)
+      return fail(SLORA_E_INVAL, f + ": workspace must be non-NULL and 16-byte aligned");
+    if (workspace_bytes < st->workspace()) return fail(SLORA_E_NOMEM, f + ": workspace smaller than workspace_bytes");
+  }
+  if (!st->dev) return fail(SLORA_E_INVAL, f + ": step not uploaded (call slora_kv_step_upload)");
+  if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
+  KvAttend A{};
+  A.kv = kv->view();
+  A.tiles = reinterpret_cast<const KvTile*>(st->dev + st->tiles_off());
+  A.prompts = reinterpret_cast<const KvTile*>(st->dev + st->prompts_off());
+  A.n_prompts = (int32_t)st->prompts.size();
+  A.n_tiles = (int32_t)st->tiles.size();
+  A.combine = A.tiles + A.n_tiles;
+  A.counters = reinterpret_cast<uint32_t*>(const_cast<char*>(st->dev + st->counters_off()));
+  A.n_combine = (int32_t)st->combine.size();
+  A.layer = layer;
+  A.window = window;
+  A.sinks = window ? std::min(sinks, kv->d.max_tokens) : 0;    // without a window all are visible
+  A.q = q;
+  A.out = out;
+  A.q_stride = q_stride;
+  A.out_stride = out_stride;
+  A.scale_log2 = scale_log2;
+  A.part = static_cast<float*>(workspace);
+  return launched(f, launch_kv_attend(A, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -417,9 +462,15 @@ slora_status slora_kv_pages(const slora_kv* kv, int32_t seq, int32_t layer, int3
 
 slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, const int32_t* counts, int32_t reread,
                                  slora_kv_step** out) {
+  return slora_kv_build_step_window(kv, n, seqs, counts, reread, 0, 0, out);
+}
+
+slora_status slora_kv_build_step_window(slora_kv* kv, int32_t n, const int32_t* seqs, const int32_t* counts,
+                                        int32_t reread, int32_t window, int32_t sinks, slora_kv_step** out) {
   if (!kv || !out || n < 0 || (n > 0 && (!seqs || !counts)))
     return fail(SLORA_E_INVAL, "slora_kv_build_step: NULL argument");
   if (reread != 0 && reread != 1) return fail(SLORA_E_INVAL, "slora_kv_build_step: reread must be 0 or 1");
+  if (window < 0 || sinks < 0) return fail(SLORA_E_INVAL, "slora_kv_build_step: window and sinks must not be negative");
   slora_kv_step* st = nullptr;
   try {
     std::vector<uint8_t> named((size_t)kv->d.max_seqs, 0);
@@ -465,7 +516,7 @@ slora_status slora_kv_build_step(slora_kv* kv, int32_t n, const int32_t* seqs, c
     st->n_small = (int32_t)(std::stable_partition(st->blocks.begin(), st->blocks.end(), [](const KvBlock& b) {
                               return b.slot1 - b.slot0 == 1;
                             }) - st->blocks.begin());
-    build_tiles(st);
+    build_tiles(st, window, sinks);
     // a launch holds fewer than 2^32 threads, and counts in the kernels are 31 bits
     constexpr int64_t kMostGroups = ((int64_t)1 << 32) / kThreads - 1;
     const int64_t kvh = kv->d.n_kv_heads;
@@ -660,41 +711,15 @@ slora_status slora_kv_rotary_table(slora_kv* kv, const slora_kv_rotary* r, int64
 slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* st, int32_t layer, const void* q, int64_t q_stride,
                              void* out, int64_t out_stride, float scale, int32_t window, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  const std::string f = "slora_kv_attend";
-  slora_status ok = check_launch(f, kv, st, layer);
-  if (ok != SLORA_OK) return ok;
-  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
-  if (!std::isfinite(scale_log2)) return fail(SLORA_E_INVAL, f + ": scale times log2(e) must be finite in fp32");
-  if (window < 0) return fail(SLORA_E_INVAL, f + ": window must be 0 (none) or positive");
-  if (st->n_rows == 0) return SLORA_OK;
-  if (!q || !out) return fail(SLORA_E_INVAL, f + ": NULL q or out");
-  if ((ok = check_rows(f, "q", kv, q, q_stride, kv->d.n_heads)) != SLORA_OK) return ok;
-  if ((ok = check_rows(f, "out", kv, out, out_stride, kv->d.n_heads)) != SLORA_OK) return ok;
-  if (st->workspace() > 0) {
-    if (!workspace || reinterpret_cast<uintptr_t>(workspace) & 15)
-      return fail(SLORA_E_INVAL, f + ": workspace must be non-NULL and 16-byte aligned");
-    if (workspace_bytes < st->workspace()) return fail(SLORA_E_NOMEM, f + ": workspace smaller than workspace_bytes");
-  }
-  if (!st->dev) return fail(SLORA_E_INVAL, f + ": step not uploaded (call slora_kv_step_upload)");
-  if ((ok = pool_device_current(kv->pool)) != SLORA_OK) return ok;
-  KvAttend A{};
-  A.kv = kv->view();
-  A.tiles = reinterpret_cast<const KvTile*>(st->dev + st->tiles_off());
-  A.prompts = reinterpret_cast<const KvTile*>(st->dev + st->prompts_off());
-  A.n_prompts = (int32_t)st->prompts.size();
-  A.n_tiles = (int32_t)st->tiles.size();
-  A.combine = A.tiles + A.n_tiles;
-  A.counters = reinterpret_cast<uint32_t*>(const_cast<char*>(st->dev + st->counters_off()));
-  A.n_combine = (int32_t)st->combine.size();
-  A.layer = layer;
-  A.window = window;
-  A.q = q;
-  A.out = out;
-  A.q_stride = q_stride;
-  A.out_stride = out_stride;
-  A.scale_log2 = scale_log2;
-  A.part = static_cast<float*>(workspace);
-  return launched(f, launch_kv_attend(A, static_cast<hipStream_t>(stream)));
+  return attend("slora_kv_attend", kv, st, layer, q, q_stride, out, out_stride, scale, window, 0, workspace,
+                workspace_bytes, stream);
+}
+
+slora_status slora_kv_attend_sinks(slora_kv* kv, const slora_kv_step* st, int32_t layer, const void* q,
+                                   int64_t q_stride, void* out, int64_t out_stride, float scale, int32_t window,
+                                   int32_t sinks, void* workspace, size_t workspace_bytes, void* stream) {
+  return attend("slora_kv_attend_sinks", kv, st, layer, q, q_stride, out, out_stride, scale, window, sinks, workspace,
+                workspace_bytes, stream);
 }
 
 slora_status slora_kv_read(slora_kv* kv, const slora_kv_step* st, int32_t layer, void* k, int64_t k_stride, void* v,

@@ -48,7 +48,7 @@ EXPORTED = [
     "slora_kv_device_bytes", "slora_kv_create", "slora_kv_destroy", "slora_kv_drop", "slora_kv_length",
     "slora_kv_pages", "slora_kv_build_step", "slora_kv_step_destroy", "slora_kv_step_get_info",
     "slora_kv_step_upload", "slora_kv_append", "slora_kv_attend", "slora_kv_read",
-    "slora_kv_append_norm", "slora_kv_rotary_table",
+    "slora_kv_append_norm", "slora_kv_rotary_table", "slora_kv_build_step_window", "slora_kv_attend_sinks",
 ]
 # include/slora_probe.h: bandwidth probes (measurement only)
 EXPORTED_PROBE = ["slora_probe_read", "slora_probe_gather"]
@@ -173,6 +173,8 @@ def lib():
             "slora_kv_pages": (c_int32, [P, c_int32, c_int32, c_int32, POINTER(c_int32), c_int32, POINTER(c_int32)]),
             "slora_kv_build_step": (c_int32, [P, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32,
                                               POINTER(KvStep)]),
+            "slora_kv_build_step_window": (c_int32, [P, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32, c_int32,
+                                                     c_int32, POINTER(KvStep)]),
             "slora_kv_step_destroy": (None, [P]),
             "slora_kv_step_get_info": (c_int32, [P, POINTER(KvStepInfo)]),
             "slora_kv_step_upload": (c_int32, [P, P, c_size_t, P]),
@@ -182,6 +184,8 @@ def lib():
                                                POINTER(KvNorm), P, c_int64, P]),
             "slora_kv_rotary_table": (c_int32, [P, POINTER(KvRotary), c_int64, c_int64, P, P]),
             "slora_kv_attend": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, c_float, c_int32, P, c_size_t, P]),
+            "slora_kv_attend_sinks": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, c_float, c_int32, c_int32, P,
+                                                c_size_t, P]),
             "slora_kv_read": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, P]),
             "slora_probe_read": (c_int32, [P, c_int64, c_int32, c_int32, P, P, P, P]),
             "slora_probe_gather": (c_int32, [P, c_int64, c_int64, P, c_int64, P, c_int64, c_int64, P,
@@ -583,15 +587,18 @@ def slora_kv_pages(kv, seq: int, layer: int = 0, head: int = 0) -> np.ndarray:
     return ids[:n.value]
 
 
-def slora_kv_build_step(kv, seqs, counts, reread: bool = False) -> KvStep:
+def slora_kv_build_step(kv, seqs, counts, reread: bool = False, window: int = 0, sinks: int = 0) -> KvStep:
+    """window, sinks: what its attention will see, where that is a window and the first tokens (the work is cut for it)."""
     seqs = np.ascontiguousarray(seqs, dtype=np.int32)
     counts = np.ascontiguousarray(counts, dtype=np.int32)
     if seqs.ndim != 1 or seqs.shape != counts.shape:
         raise ValueError("one count per sequence")
     step = KvStep()
-    _check(lib().slora_kv_build_step(kv, seqs.size, _i32p(seqs) if seqs.size else None,
-                                     _i32p(counts) if seqs.size else None, int(reread), ctypes.byref(step)),
-           "slora_kv_build_step")
+    args = (kv, seqs.size, _i32p(seqs) if seqs.size else None, _i32p(counts) if seqs.size else None, int(reread))
+    if window or sinks:
+        _check(lib().slora_kv_build_step_window(*args, window, sinks, ctypes.byref(step)), "slora_kv_build_step_window")
+    else:
+        _check(lib().slora_kv_build_step(*args, ctypes.byref(step)), "slora_kv_build_step")
     step.kv, step.n_rows, step.dim = kv, int(counts.sum(dtype=np.int64)), kv.desc.head_dim
     return step
 
@@ -733,6 +740,19 @@ def slora_kv_attend(kv, step, layer: int, q, out, scale: float, window: int = 0,
                                     _stream(stream))
     if status:
         _check(status, "slora_kv_attend")
+
+
+def slora_kv_attend_sinks(kv, step, layer: int, q, out, scale: float, window: int, sinks: int, workspace=None,
+                          workspace_bytes: int = 0, stream=None, q_stride=None, out_stride=None) -> None:
+    """slora_kv_attend over the window and the first `sinks` tokens."""
+    heads = kv.heads[0]
+    qp, qs = _rows(q, step, heads, q_stride)
+    op, os_ = _rows(out, step, heads, out_stride)
+    workspace = _area(workspace, workspace_bytes, kv.device, "workspace")
+    status = kv.api.slora_kv_attend_sinks(kv, step, layer, qp, qs, op, os_, scale, window, sinks, workspace,
+                                          int(workspace_bytes), _stream(stream))
+    if status:
+        _check(status, "slora_kv_attend_sinks")
 
 
 def slora_kv_read(kv, step, layer: int, k=None, v=None, stream=None, k_stride=None, v_stride=None) -> None:
