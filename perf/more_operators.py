@@ -319,6 +319,9 @@ def _prepare_own(st, past, seed):
     made = _back(case) if case["op"] == "take" else []
     S, kv = _cache_own(st, case, (blocks + sum(-(-n // bt) for n, _ in made)) * hk * case["layers"],
                        seed, max_seqs=len(lens) + len(made), max_tokens=max(c + r for c, r in lens))
+    if case["op"] == "sinks":                          # the rows are cached too: all tokens arrive together
+        past = [torch.cat([_joined(lens, past[0][:, :hk], st["k"]), _joined(lens, past[0][:, hk:], st["v"])], 1)]
+        ctx = [c + r for c, r in lens]
     if sum(ctx):
         s, _ = _step(st, list(range(len(lens))), ctx)
         for layer, x in enumerate(past):
@@ -336,8 +339,7 @@ def _prepare_own(st, past, seed):
         _take_own(st)                                  # how much metadata the read back takes
         return st
     if case["op"] == "sinks":
-        st["step"], info = _step(st, list(range(len(lens))), rows, window=case["window"], sinks=case["sinks"])
-        S.slora_kv_append(kv, st["step"], 0, st["k"], st["v"], stream=torch.cuda.current_stream())
+        st["step"], info = _step(st, list(range(len(lens))), rows, True, window=case["window"], sinks=case["sinks"])
         st["workspace"] = torch.empty(max(16, info["workspace_bytes"]), dtype=torch.uint8, device=DEV)
     else:
         st["step"], _ = _step(st, list(range(len(lens))), rows)
