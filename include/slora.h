@@ -500,8 +500,8 @@ const char* slora_last_error(void);
  * beyond fp32) makes the range NaN, and every key (or value) of that block and
  * head then reads as NaN: it is never lost silently.
  *
- * Position p of a sequence is its p-th token (0, 1, ...).  Rotation by
- * positions: for the pairs (a_i, b_i), i = 0 .. rot_dim/2 - 1, of a head,
+ * Position p of a sequence is its p-th token (0, 1, ...), until slora_kv_take
+ * leaves tokens out: the others keep theirs.  Rotation by positions: for the pairs (a_i, b_i), i = 0 .. rot_dim/2 - 1, of a head,
  *
  *     a_i' = a_i cos(p, i) - b_i sin(p, i)     b_i' = b_i cos(p, i) + a_i sin(p, i)
  *
@@ -569,6 +569,9 @@ void slora_kv_destroy(slora_kv* kv);
  * steps built with it become stale.  Launches that still read the pages must
  * be ordered before whatever the caller lets write them next. */
 slora_status slora_kv_drop(slora_kv* kv, int32_t seq);
+/* The position of sequence `seq`'s next token: its length, and what slora_kv_take
+ * left out before its last token; -1 on a bad argument. */
+int64_t slora_kv_position(const slora_kv* kv, int32_t seq);
 /* Tokens of sequence `seq` (with those of every step built so far), or -1. */
 int64_t slora_kv_length(const slora_kv* kv, int32_t seq);
 /* Page ids of sequence `seq`, layer, kv head, block by block: the first
@@ -714,6 +717,49 @@ slora_status slora_kv_attend(slora_kv* kv, const slora_kv_step* step, int32_t la
 slora_status slora_kv_attend_sinks(slora_kv* kv, const slora_kv_step* step, int32_t layer, const void* q,
                                    int64_t q_stride, void* out, int64_t out_stride, float scale, int32_t window,
                                    int32_t sinks, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sequences made of other sequences' tokens, in every layer: for i = 0 .. n-1,
+ * sequence dst[i] becomes the tokens of sequence src[i] in n_ranges[i] ranges
+ * [first, last) of its tokens, in their order.  ranges holds the (first, last)
+ * pairs of all, those of dst[0] first: ascending, not overlapping, within
+ * src[i]'s length; empty ones count for nothing.
+ *
+ *  - dst[i] != src[i]: a fork.  dst[i] is empty before, src[i] stays as it is.
+ *    One range [0, length) copies the whole sequence: another answer to the same
+ *    prompt.
+ *  - dst[i] == src[i]: the tokens outside the ranges are dropped, and what they
+ *    alone used goes to the tail of the pool's free list.  One range [0, n) takes
+ *    tokens back (of a draft that was refused); [0, sinks) and [length - window,
+ *    length) bound what a long conversation holds.
+ *
+ * A block of dst[i] that is whole and holds the tokens of one whole block of
+ * src[i] shares that block's pages: it takes no memory and no time, and the pages
+ * are freed with the last sequence that holds them.  (So ranges that begin and
+ * end at multiples of block_tokens move nothing.)  In place, a last block that
+ * only lost its end keeps its pages too.  All other blocks are written to pages of their own, taken from the
+ * pool for every layer and kv head, all or nothing (SLORA_E_NOMEM): the range of such a block is the
+ * largest of the ranges of the blocks that its tokens come from (of keys and of
+ * values; NaN where one is), and codes of smaller ones are coded again, as where
+ * an append raises a range.
+ *
+ * Tokens are renumbered 0, 1, ..., for windows, sinks and everything else
+ * but the rotation: a token keeps the position that it was rotated by, and the
+ * next one's is one more than the last token's (slora_kv_position).
+ *
+ * A token has to have been appended in every layer (SLORA_E_INVAL).  No sequence
+ * that the call changes may be another one's source.  Steps built with dst[i]
+ * become stale.  A block that sequences share takes no further appends, repeats
+ * and replays included; none is ever partly filled.  Uploads to dev_meta (device,
+ * at least slora_kv_take_bytes, 16-byte aligned, kept untouched until the launches
+ * are done) and launches on `stream`, without waiting; ordered as uploads and
+ * launches are, and launches that still read freed pages must be ordered before
+ * whatever the caller lets write them next.  Refused while `stream` is captured. */
+slora_status slora_kv_take(slora_kv* kv, int32_t n, const int32_t* dst, const int32_t* src, const int32_t* n_ranges,
+                           const int64_t* ranges, void* dev_meta, size_t dev_meta_bytes, void* stream);
+/* Bytes of device metadata that such a call needs as things stand; 0 on a bad
+ * argument. */
+size_t slora_kv_take_bytes(const slora_kv* kv, int32_t n, const int32_t* dst, const int32_t* src,
+                           const int32_t* n_ranges, const int64_t* ranges);
 
 /* Read the cached keys and values of the step's rows in `layer` back, as the
  * values their codes stand for (keys as they were stored: rotated), rounded

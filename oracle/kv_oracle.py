@@ -98,7 +98,43 @@ class KvModel:
     def __init__(self, code, n_heads, n_kv, dim, block, rot=0, pairs=HALVES, cs=None):
         self.code, self.n_heads, self.n_kv, self.dim, self.block = code, n_heads, n_kv, dim, block
         self.rot, self.pairs, self.cs = rot, pairs, cs
-        self.codes, self.range = {}, {}
+        self.codes, self.range, self.skipped = {}, {}, {}
+
+    def position(self, seq, layer=0):
+        """The rotation's position of the sequence's next token: tokens that were left out before it count."""
+        n, runs = self.length(seq, layer), self.skipped.get((seq, layer))
+        return n if runs is None or not len(runs) else int(runs[-1]) + 1 + n - len(runs)
+
+    def take(self, made):
+        """made: (dst, src, ranges) of each sequence that becomes tokens of another or of itself, in every layer."""
+        old = (dict(self.codes), dict(self.range), {k: self._positions(*k[:2]) for k in self.codes})
+        for dst, src, ranges in made:
+            for layer in {key[1] for key in self.codes}:
+                if (src, layer, 0) not in old[0]:
+                    continue
+                at = np.concatenate([np.arange(a, b) for a, b in ranges] + [np.zeros(0, int)]).astype(int)
+                for what in (0, 1):
+                    key = (src, layer, what)
+                    held = old[1][key][at // self.block] if at.size else np.zeros((0, self.n_kv))
+                    grown = np.array([held[i:i + self.block].max(0) for i in range(0, at.size, self.block)])
+                    grown = grown.reshape(-1, self.n_kv)                       # (max keeps NaN)
+                    now = grown[np.arange(at.size) // self.block]
+                    with np.errstate(invalid="ignore", divide="ignore"):
+                        ratio = np.where(now > 0, held / now, 1.0)[:, :, None]
+                    codes = nearest(self.code, old[0][key][at] * ratio)
+                    codes[np.isnan(now)] = 0
+                    self.codes[dst, layer, what], self.range[dst, layer, what] = codes, grown
+                self.skipped[dst, layer] = old[2][key][at]
+
+    def _positions(self, seq, layer):
+        runs, n = self.skipped.get((seq, layer), np.zeros(0, int)), self.length(seq, layer)
+        first = runs[-1] + 1 if len(runs) else 0
+        return np.concatenate([runs[:n], first + np.arange(max(0, n - len(runs)))]).astype(int)
+
+    def drop(self, seq):
+        for store in (self.codes, self.range, self.skipped):
+            for key in [k for k in store if k[0] == seq]:
+                del store[key]
 
     def length(self, seq, layer=0):
         return self.codes[seq, layer, 0].shape[0] if (seq, layer, 0) in self.codes else 0
@@ -107,8 +143,7 @@ class KvModel:
         return rotate(x, self.cs[start:start + len(x)] if self.rot else None, self.rot, self.pairs)
 
     def append(self, seq, layer, k, v):
-        start = self.length(seq, layer)
-        self._store(seq, layer, 0, self.rotated(k, start))
+        self._store(seq, layer, 0, self.rotated(k, self.position(seq, layer)))
         self._store(seq, layer, 1, np.asarray(v, np.float64))
 
     def _store(self, seq, layer, what, x):

@@ -1406,6 +1406,21 @@ bool slora::pool_info(const slora_pool* p, PoolInfo* info) {
   return true;
 }
 
+void slora::pool_untake_pages(slora_pool* p, int32_t cls, int64_t n, const int32_t* ids) {
+  for (int64_t i = n - 1; i >= 0; --i) {
+    p->state[cls][ids[i]] = PAGE_FREE;
+    p->free_list[cls].push_front(ids[i]);
+  }
+}
+
+void slora::pool_return_pages(slora_pool* p, int32_t cls, int64_t n, const int32_t* ids) {
+  for (int64_t i = 0; i < n; ++i) {
+    if (p->state[cls][ids[i]] != PAGE_KV) continue;            // the caller has freed it by hand
+    p->state[cls][ids[i]] = PAGE_FREE;
+    p->free_list[cls].push_back(ids[i]);
+  }
+}
+
 slora_status slora::pool_upload(slora_pool* p, void* dst, const void* src, size_t bytes, hipStream_t stream) {
   slora_status st = set_device(p);
   if (st != SLORA_OK) return st;

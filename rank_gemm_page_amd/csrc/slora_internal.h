@@ -25,6 +25,10 @@ bool pool_info(const slora_pool* pool, PoolInfo* info);
 // Queue a copy of host bytes to dst on `stream` through the pool's pinned
 // metadata slots (src may be reused at once).
 slora_status pool_upload(slora_pool* pool, void* dst, const void* src, size_t bytes, hipStream_t stream);
+// KV pages that a call took and holds: back to the head of the free list, as if it
+// had never taken them, or to its tail.  Neither can fail.
+void pool_untake_pages(slora_pool* pool, int32_t cls, int64_t n, const int32_t* ids);
+void pool_return_pages(slora_pool* pool, int32_t cls, int64_t n, const int32_t* ids);
 // Workspace bytes one projection of the batch needs (slora_segments_info.workspace_bytes).
 size_t segments_workspace_bytes(const slora_segments* seg);
 

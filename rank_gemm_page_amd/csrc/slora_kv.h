@@ -35,8 +35,9 @@ struct KvView {
 };
 
 // Records of a step (device metadata, int32 words).
-// A touched block: sequence id, block, its slots [slot0, slot1) among the rows, batch row of slot0.
-struct KvBlock { int32_t seq, block, slot0, slot1, row, pad[3]; };
+// A touched block: sequence id, block, its slots [slot0, slot1) among the rows, batch row of slot0, and how far the
+// rotation's positions of the rows are from their places.
+struct KvBlock { int32_t seq, block, slot0, slot1, row, shift, pad[2]; };
 // A tile of a sequence's packed rows: number, key split of how many, slots (see below); and the sequence: its first
 // row's position, its rows, the batch row of the first.
 struct KvTile { int32_t seq, tile, split, splits, part, start, rows, row0; };
@@ -96,6 +97,23 @@ struct KvRotary {
   int32_t half, run;          // run: positions of a thread
 };
 
+// Sequences made of others' tokens.  The page table rows of sequence dst from block `first` on: n entries, of which
+// entries[at + i] is the block of src whose page it shares, or ~c for the pages of copy c.
+struct KvTakeRow { int32_t dst, src, first, n, at, pad[3]; };
+// A block written anew: `count` tokens of src, at tokens[at ..].
+struct KvCopy { int32_t src, count, at, pad; };
+struct KvTake {
+  KvView kv;
+  const KvTakeRow* rows;
+  const KvCopy* copies;
+  const int32_t* entries;
+  const int32_t* tokens;
+  const int32_t* pages;       // [copy][layer][head]
+  int32_t n_rows, n_copies;
+  int64_t first;              // work before this is done by another launch (set by the launch)
+};
+
+hipError_t launch_kv_take(const KvTake& A, bool in_place, hipStream_t stream);
 hipError_t launch_kv_rotary(const KvRotary& R, hipStream_t stream);
 hipError_t launch_kv_patch(int32_t* table, const KvPatch* patches, int32_t n, hipStream_t stream);
 hipError_t launch_kv_append(const KvAppend& A, bool norm, hipStream_t stream);

@@ -29,9 +29,53 @@ struct Seq {
   int32_t blocks = 0;      // blocks of one layer and head
   int32_t entered = 0;     // of these, in the device's page table
   uint64_t gen = 0;        // counts drops
-  std::vector<int32_t> pages;   // [block][layer][head]
+  std::vector<int32_t> held;    // [block] record of its pages
   std::vector<int32_t> stored;  // [block][layer] tokens that appends have been launched for
+  // from token first on, the rotation's position is the token's number + shift (no runs: 0)
+  struct Run { int32_t first, shift; };
+  std::vector<Run> runs;
+  int32_t shift() const { return runs.empty() ? 0 : runs.back().shift; }
 };
+
+// The pages of blocks, [layer][head] of each, and how many sequences hold it.  A
+// block that more than one holds is full, and nothing writes to it.
+struct Blocks {
+  std::vector<int32_t> pages, refs, spare;
+  size_t room = 0;
+  // Room for n more, after which add and release cannot fail.
+  void reserve(int64_t n, int64_t per) {
+    const size_t want = refs.size() + (size_t)std::max<int64_t>(0, n - (int64_t)spare.size());
+    if (want <= room) return;
+    const size_t grown = std::max(want, 2 * room);
+    pages.reserve(grown * (size_t)per);
+    spare.reserve(grown);
+    refs.reserve(grown);
+    room = grown;
+  }
+  int32_t add(const int32_t* ids, int64_t per) {
+    int32_t at = (int32_t)refs.size();
+    if (spare.empty()) {
+      refs.push_back(1);
+      pages.insert(pages.end(), ids, ids + per);
+    } else {
+      at = spare.back();
+      spare.pop_back();
+      refs[at] = 1;
+      std::copy(ids, ids + per, pages.begin() + at * per);
+    }
+    return at;
+  }
+  // Whether the last holder let go of it.
+  bool release(int32_t at) {
+    if (--refs[at]) return false;
+    spare.push_back(at);
+    return true;
+  }
+};
+
+constexpr int64_t kMostPositions = (int64_t)1 << 30;
+// a launch holds fewer than 2^32 threads, and counts in the kernels are 31 bits
+constexpr int64_t kMostGroups = ((int64_t)1 << 32) / kThreads - 1;
 
 // Checks a description against a pool; the block size and blocks of the
 // longest sequence on success, a message otherwise.
@@ -77,7 +121,9 @@ struct slora_kv {
   int32_t block = 0, max_blocks = 0;
   char* dev = nullptr;
   std::vector<Seq> seqs;
+  Blocks blocks;
 
+  const int32_t* pages_of(int32_t record) const { return blocks.pages.data() + record * per_block(); }
   int32_t elem() const { return info.dtype == SLORA_F16 ? 2 : 4; }
   int64_t per_block() const { return (int64_t)d.n_layers * d.n_kv_heads; }
   int32_t* table() const { return reinterpret_cast<int32_t*>(dev); }
@@ -267,6 +313,8 @@ slora_status check_order(const std::string& f, const slora_kv* kv, const slora_k
       return fail(SLORA_E_INVAL, f + ": earlier tokens of a block have not been appended in this layer");
     if (have > b.slot1)
       return fail(SLORA_E_INVAL, f + ": later tokens of a block have been appended in this layer");
+    if (kv->blocks.refs[kv->seqs[b.seq].held[b.block]] > 1)
+      return fail(SLORA_E_INVAL, f + ": another sequence shares a block of the step");
   }
   return SLORA_OK;
 }
@@ -376,6 +424,124 @@ slora_status attend(const std::string& f, slora_kv* kv, const slora_kv_step* st,
   return launched(f, launch_kv_attend(A, static_cast<hipStream_t>(stream)));
 }
 
+// What a call of slora_kv_take does: the device's records, and what its sequences
+// are afterwards.
+struct TakePlan {
+  struct Part {
+    int32_t dst, src;
+    int64_t len = 0;
+    std::vector<int32_t> from;     // [block] the block of src whose pages it shares, or ~copy
+    std::vector<Seq::Run> runs;
+  };
+  std::vector<Part> parts;
+  std::vector<KvTakeRow> rows;
+  std::vector<KvCopy> copies;
+  std::vector<int32_t> entries, tokens;
+  bool in_place = false;           // a launch of copies reads rows that the call changes
+  int64_t per = 0;
+
+  size_t copies_off() const { return rows.size() * sizeof(KvTakeRow); }
+  size_t entries_off() const { return copies_off() + copies.size() * sizeof(KvCopy); }
+  size_t tokens_off() const { return entries_off() + entries.size() * sizeof(int32_t); }
+  size_t pages_off() const { return tokens_off() + tokens.size() * sizeof(int32_t); }
+  size_t bytes() const { return pages_off() + copies.size() * (size_t)per * sizeof(int32_t); }
+};
+
+// The plan of a call; a message if it is refused.  (Throws std::bad_alloc.)
+const char* plan_take(const slora_kv* kv, int32_t n, const int32_t* dst, const int32_t* src, const int32_t* n_ranges,
+                      const int64_t* ranges, TakePlan* plan) {
+  if (!kv || n < 0 || (n > 0 && (!dst || !src || !n_ranges))) return "NULL argument";
+  plan->per = kv->per_block();
+  std::vector<uint8_t> changed((size_t)kv->d.max_seqs, 0);
+  for (int32_t i = 0; i < n; ++i) {
+    if (dst[i] < 0 || dst[i] >= kv->d.max_seqs || src[i] < 0 || src[i] >= kv->d.max_seqs)
+      return "sequence id out of range";
+    if (changed[dst[i]]++) return "a sequence is made twice";
+    if (n_ranges[i] < 0 || (n_ranges[i] > 0 && !ranges)) return "NULL or negative ranges";
+  }
+  const int32_t bt = kv->block, layers = kv->d.n_layers;
+  int64_t at = 0;
+  std::vector<std::pair<int64_t, int64_t>> kept;               // ranges, those that touch joined
+  for (int32_t i = 0; i < n; ++i) {
+    const bool same = dst[i] == src[i];
+    if (!same && changed[src[i]]) return "the source of a sequence is changed by the same call";
+    const Seq& s = kv->seqs[src[i]];
+    if (!same && kv->seqs[dst[i]].blocks) return "a sequence that is made from another one must be empty";
+    kept.clear();
+    int64_t end = 0;
+    TakePlan::Part part;
+    part.dst = dst[i];
+    part.src = src[i];
+    for (int32_t r = 0; r < n_ranges[i]; ++r, ++at) {
+      const int64_t lo = ranges[2 * at], hi = ranges[2 * at + 1];
+      if (lo < end || hi < lo || hi > s.len) return "ranges must ascend within the sequence's tokens";
+      end = hi;
+      if (lo == hi) continue;
+      for (int64_t b = lo / bt; b * bt < hi; ++b) {
+        if (b >= s.entered) return "the step of a token has not been uploaded";
+        for (int32_t layer = 0; layer < layers; ++layer)
+          if (s.stored[(size_t)b * layers + layer] < std::min<int64_t>(bt, hi - b * bt))
+            return "a token has not been appended in every layer";
+      }
+      if (!kept.empty() && kept.back().second == lo) kept.back().second = hi;
+      else kept.push_back({lo, hi});
+    }
+    // positions: the source's runs, cut by the ranges
+    size_t run = 0;
+    for (const auto& k : kept) {
+      for (int64_t p = k.first; p < k.second;) {
+        while (run + 1 < s.runs.size() && s.runs[run + 1].first <= p) ++run;
+        const bool last = run + 1 >= s.runs.size();
+        const int64_t stop = last ? k.second : std::min<int64_t>(k.second, s.runs[run + 1].first);
+        // a run holds from its first token on; before the first of all there is no shift
+        const int32_t shift = s.runs.empty() ? 0 : s.runs[run].shift;
+        const Seq::Run made = {(int32_t)part.len, (int32_t)(p + shift - part.len)};
+        if (part.runs.empty() || part.runs.back().shift != made.shift) part.runs.push_back(made);
+        part.len += stop - p;
+        p = stop;
+      }
+    }
+    // blocks
+    size_t k = 0;
+    int64_t p = kept.empty() ? 0 : kept[0].first;
+    for (int64_t left = part.len; left > 0;) {
+      const int64_t count = std::min<int64_t>(bt, left), block = p / bt;
+      left -= count;
+      const bool alike = p % bt == 0 && kept[k].second - p >= count;
+      if (alike && (count == bt || (same && kv->blocks.refs[s.held[block]] == 1))) {
+        part.from.push_back((int32_t)block);
+        p += count;
+      } else {
+        part.from.push_back(~(int32_t)plan->copies.size());
+        plan->copies.push_back({src[i], (int32_t)count, (int32_t)plan->tokens.size(), 0});
+        if (same) plan->in_place = true;
+        for (int64_t want = count; want > 0;) {
+          const int64_t take = std::min(want, kept[k].second - p);
+          for (int64_t t = 0; t < take; ++t) plan->tokens.push_back((int32_t)(p + t));
+          want -= take;
+          p += take;
+          if (p == kept[k].second && want > 0) p = kept[++k].first;
+        }
+        if (plan->tokens.size() > (size_t)INT32_MAX / 2) return "the call is too large for one launch";
+      }
+      if (left > 0 && p == kept[k].second) p = kept[++k].first;
+    }
+    int32_t first = 0;                                         // what stays where it is
+    const int32_t blocks = (int32_t)part.from.size();
+    while (same && first < blocks && part.from[first] == first) ++first;
+    if (first < blocks) {
+      plan->rows.push_back({dst[i], src[i], first, blocks - first, (int32_t)plan->entries.size(), {0, 0, 0}});
+      plan->entries.insert(plan->entries.end(), part.from.begin() + first, part.from.end());
+    }
+    plan->parts.push_back(std::move(part));
+    if (plan->entries.size() > (size_t)INT32_MAX / 2) return "the call is too large for one launch";
+  }
+  if ((double)(plan->copies.size() + plan->rows.size()) * plan->per > kMostGroups ||
+      (double)plan->copies.size() * plan->per > INT32_MAX / 2)
+    return "the call is too large for one launch";
+  return nullptr;
+}
+
 }  // namespace
 
 extern "C" {
@@ -422,14 +588,20 @@ slora_status slora_kv_drop(slora_kv* kv, int32_t seq) {
   if (seq < 0 || seq >= kv->d.max_seqs) return fail(SLORA_E_INVAL, "slora_kv_drop: sequence id out of range");
   Seq& s = kv->seqs[seq];
   try {
-    slora_status st = slora_free_pages(kv->pool, kv->d.cls, (int64_t)s.pages.size(), s.pages.data());
+    std::vector<int32_t> alone;                                // pages that no other sequence holds
+    for (int32_t record : s.held)
+      if (kv->blocks.refs[record] == 1)
+        alone.insert(alone.end(), kv->pages_of(record), kv->pages_of(record) + kv->per_block());
+    slora_status st = slora_free_pages(kv->pool, kv->d.cls, (int64_t)alone.size(), alone.data());
     if (st != SLORA_OK) return st;
   } catch (const std::bad_alloc&) {
     return fail(SLORA_E_NOMEM, "slora_kv_drop: out of host memory");
   }
-  s.pages.clear();
-  s.pages.shrink_to_fit();
+  for (int32_t record : s.held) (void)kv->blocks.release(record);
+  s.held.clear();
+  s.held.shrink_to_fit();
   s.stored.clear();
+  s.runs.clear();
   s.len = 0;
   s.blocks = s.entered = 0;
   ++s.gen;
@@ -441,6 +613,11 @@ void slora_kv_destroy(slora_kv* kv) {
   for (int32_t i = 0; i < kv->d.max_seqs; ++i)
     if (kv->seqs[i].blocks) (void)slora_kv_drop(kv, i);
   delete kv;
+}
+
+int64_t slora_kv_position(const slora_kv* kv, int32_t seq) {
+  if (!kv || seq < 0 || seq >= kv->d.max_seqs) return -1;
+  return kv->seqs[seq].len + kv->seqs[seq].shift();
 }
 
 int64_t slora_kv_length(const slora_kv* kv, int32_t seq) {
@@ -455,7 +632,7 @@ slora_status slora_kv_pages(const slora_kv* kv, int32_t seq, int32_t layer, int3
     return fail(SLORA_E_INVAL, "slora_kv_pages: sequence, layer or head out of range");
   const Seq& s = kv->seqs[seq];
   for (int32_t b = 0; b < std::min(cap, s.blocks); ++b)
-    ids[b] = s.pages[(size_t)(b * kv->per_block() + (int64_t)layer * kv->d.n_kv_heads + head)];
+    ids[b] = kv->pages_of(s.held[b])[(int64_t)layer * kv->d.n_kv_heads + head];
   *n = s.blocks;
   return SLORA_OK;
 }
@@ -485,6 +662,8 @@ slora_status slora_kv_build_step_window(slora_kv* kv, int32_t n, const int32_t* 
         return fail(SLORA_E_INVAL, "slora_kv_build_step: more rows than the sequence has tokens");
       if (!reread && len + counts[i] > kv->d.max_tokens)
         return fail(SLORA_E_INVAL, "slora_kv_build_step: a sequence would pass max_tokens");
+      if (!reread && len + counts[i] + kv->seqs[seqs[i]].shift() > kMostPositions)
+        return fail(SLORA_E_INVAL, "slora_kv_build_step: a sequence would pass position 2^30");
       rows += counts[i];
     }
     if (rows > INT32_MAX / 2) return fail(SLORA_E_INVAL, "slora_kv_build_step: too many rows");
@@ -503,22 +682,21 @@ slora_status slora_kv_build_step_window(slora_kv* kv, int32_t n, const int32_t* 
       st->gens.push_back(s.gen);
       st->ends.push_back(blocks);
       st->max_len = std::max(st->max_len, (int32_t)end);
-      if (counts[i]) st->n_positions = std::max(st->n_positions, (int32_t)end);
+      const int32_t shift = reread ? 0 : s.shift();              // (a reread step rotates nothing)
+      if (counts[i]) st->n_positions = std::max(st->n_positions, (int32_t)end + shift);
       need += (blocks - s.blocks) * kv->per_block();
       patches += (blocks - s.entered) * kv->per_block();
-      for (int32_t p = start; p < end; ++p) st->row_pos.push_back(p);
+      for (int32_t p = start; p < end; ++p) st->row_pos.push_back(p + shift);
       for (int32_t b = start / kv->block; counts[i] && b < blocks; ++b)
         st->blocks.push_back({seqs[i], b, std::max(0, start - b * kv->block),
                               (int32_t)std::min<int64_t>(kv->block, end - (int64_t)b * kv->block),
-                              row0 + std::max(0, b * kv->block - start), {0, 0, 0}});
+                              row0 + std::max(0, b * kv->block - start), shift, {0, 0}});
       row0 += counts[i];
     }
     st->n_small = (int32_t)(std::stable_partition(st->blocks.begin(), st->blocks.end(), [](const KvBlock& b) {
                               return b.slot1 - b.slot0 == 1;
                             }) - st->blocks.begin());
     build_tiles(st, window, sinks);
-    // a launch holds fewer than 2^32 threads, and counts in the kernels are 31 bits
-    constexpr int64_t kMostGroups = ((int64_t)1 << 32) / kThreads - 1;
     const int64_t kvh = kv->d.n_kv_heads;
     const int64_t append =
         2 * (int64_t)st->blocks.size() * kvh + (rows * kv->d.n_heads * (kv->d.head_dim / 16)) / kThreads + 1;
@@ -534,10 +712,11 @@ slora_status slora_kv_build_step_window(slora_kv* kv, int32_t n, const int32_t* 
     }
     std::vector<int32_t> ids((size_t)need);
     st->patches.reserve((size_t)patches);
+    kv->blocks.reserve(need / kv->per_block(), kv->per_block());
     for (int32_t i = 0; i < n; ++i) {
-      std::vector<int32_t>& pages = kv->seqs[seqs[i]].pages;
-      const size_t want = (size_t)(st->ends[i] * kv->per_block());
-      if (want > pages.capacity()) pages.reserve(std::max(want, 2 * pages.capacity()));
+      std::vector<int32_t>& held = kv->seqs[seqs[i]].held;
+      const size_t want = (size_t)st->ends[i];
+      if (want > held.capacity()) held.reserve(std::max(want, 2 * held.capacity()));
       std::vector<int32_t>& stored = kv->seqs[seqs[i]].stored;
       stored.resize(std::max(stored.size(), (size_t)st->ends[i] * kv->d.n_layers), 0);
     }
@@ -551,15 +730,13 @@ slora_status slora_kv_build_step_window(slora_kv* kv, int32_t n, const int32_t* 
     size_t at = 0;
     for (int32_t i = 0; i < n; ++i) {
       Seq& s = kv->seqs[seqs[i]];
-      const size_t more = (size_t)((st->ends[i] - s.blocks) * kv->per_block());
-      s.pages.insert(s.pages.end(), ids.begin() + at, ids.begin() + at + more);
-      at += more;
-      s.blocks = st->ends[i];
+      for (; s.blocks < st->ends[i]; ++s.blocks, at += (size_t)kv->per_block())
+        s.held.push_back(kv->blocks.add(ids.data() + at, kv->per_block()));
       if (!reread) s.len += counts[i];
       for (int32_t b = s.entered; b < s.blocks; ++b)
         for (int64_t x = 0; x < kv->per_block(); ++x) {
           const uint64_t entry = ((uint64_t)seqs[i] * kv->per_block() + x) * kv->max_blocks + b;
-          const int32_t page = s.pages[(size_t)(b * kv->per_block() + x)];
+          const int32_t page = kv->pages_of(s.held[b])[x];
           st->patches.push_back({(uint32_t)entry, (uint32_t)(entry >> 32), page, 0});
         }
     }
@@ -658,7 +835,6 @@ slora_status slora_kv_rotary_table(slora_kv* kv, const slora_kv_rotary* r, int64
   const int32_t rot = kv->d.rot_dim;
   if (!rot) return fail(SLORA_E_INVAL, f + ": the cache rotates nothing (rot_dim 0)");
   if (reinterpret_cast<uintptr_t>(cos_sin) & 15) return fail(SLORA_E_INVAL, f + ": cos_sin must be 16-byte aligned");
-  constexpr int64_t kMostPositions = (int64_t)1 << 30;
   if (first < 0 || n < 0 || first > kMostPositions || n > kMostPositions - first)
     return fail(SLORA_E_INVAL, f + ": positions must be 0 .. 2^30");
   if (r->reserved0 != 0) return fail(SLORA_E_INVAL, f + ": reserved0 must be 0");
@@ -720,6 +896,116 @@ slora_status slora_kv_attend_sinks(slora_kv* kv, const slora_kv_step* st, int32_
                                    int32_t sinks, void* workspace, size_t workspace_bytes, void* stream) {
   return attend("slora_kv_attend_sinks", kv, st, layer, q, q_stride, out, out_stride, scale, window, sinks, workspace,
                 workspace_bytes, stream);
+}
+
+size_t slora_kv_take_bytes(const slora_kv* kv, int32_t n, const int32_t* dst, const int32_t* src,
+                           const int32_t* n_ranges, const int64_t* ranges) {
+  const std::string f = "slora_kv_take_bytes: ";
+  try {
+    TakePlan plan;
+    const char* why = plan_take(kv, n, dst, src, n_ranges, ranges, &plan);
+    if (!why) return std::max<size_t>(16, plan.bytes());
+    fail(SLORA_E_INVAL, f + why);
+  } catch (const std::bad_alloc&) {
+    fail(SLORA_E_NOMEM, f + "out of host memory");
+  }
+  return 0;
+}
+
+slora_status slora_kv_take(slora_kv* kv, int32_t n, const int32_t* dst, const int32_t* src, const int32_t* n_ranges,
+                           const int64_t* ranges, void* dev_meta, size_t dev_meta_bytes, void* stream) {
+  const std::string f = "slora_kv_take";
+  try {
+    TakePlan plan;
+    if (const char* why = plan_take(kv, n, dst, src, n_ranges, ranges, &plan))
+      return fail(SLORA_E_INVAL, f + ": " + why);
+    const int64_t per = plan.per, need = (int64_t)plan.copies.size() * per;
+    if (need > slora_free_count(kv->pool, kv->d.cls)) return fail(SLORA_E_NOMEM, f + ": not enough free pages");
+    const bool works = !plan.rows.empty();
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    if (works) {
+      if (!dev_meta || reinterpret_cast<uintptr_t>(dev_meta) & 15)
+        return fail(SLORA_E_INVAL, f + ": dev_meta must be non-NULL and 16-byte aligned");
+      if (dev_meta_bytes < plan.bytes()) return fail(SLORA_E_NOMEM, f + ": dev_meta smaller than slora_kv_take_bytes");
+      slora_status ok = pool_device_current(kv->pool);
+      if (ok != SLORA_OK) return ok;
+      hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+      const hipError_t e = hipStreamIsCapturing(hs, &capture);
+      if (e != hipSuccess) return fail(SLORA_E_HIP, f + ": hipStreamIsCapturing: " + hipGetErrorString(e));
+      if (capture != hipStreamCaptureStatusNone)
+        return fail(SLORA_E_INVAL, f + ": the stream is captured, which this call cannot be");
+    }
+    // everything that can run out of host memory
+    std::vector<int32_t> ids((size_t)need);
+    std::vector<char> image(works ? plan.bytes() : 0);
+    std::vector<Seq> made(plan.parts.size());
+    for (size_t i = 0; i < plan.parts.size(); ++i) {
+      const TakePlan::Part& part = plan.parts[i];
+      Seq& s = made[i];
+      s.len = part.len;
+      s.blocks = s.entered = (int32_t)part.from.size();
+      s.gen = kv->seqs[part.dst].gen + 1;
+      s.held.resize(part.from.size());
+      s.stored.assign(part.from.size() * kv->d.n_layers, kv->block);
+      if (part.len % kv->block)
+        std::fill(s.stored.end() - kv->d.n_layers, s.stored.end(), (int32_t)(part.len % kv->block));
+      s.runs = part.runs;
+    }
+    kv->blocks.reserve((int64_t)plan.copies.size(), per);
+    slora_status ok = slora_alloc_pages(kv->pool, kv->d.cls, need, ids.data());
+    if (ok != SLORA_OK) return ok;
+    if (works) {
+      auto put = [&](size_t off, const auto& v) {
+        if (!v.empty()) std::memcpy(image.data() + off, v.data(), v.size() * sizeof(v[0]));
+      };
+      put(0, plan.rows);
+      put(plan.copies_off(), plan.copies);
+      put(plan.entries_off(), plan.entries);
+      put(plan.tokens_off(), plan.tokens);
+      put(plan.pages_off(), ids);
+      ok = pool_upload(kv->pool, dev_meta, image.data(), image.size(), hs);
+      if (ok == SLORA_OK) {
+        const char* dev = static_cast<const char*>(dev_meta);
+        KvTake A{};
+        A.kv = kv->view();
+        A.rows = reinterpret_cast<const KvTakeRow*>(dev);
+        A.copies = reinterpret_cast<const KvCopy*>(dev + plan.copies_off());
+        A.entries = reinterpret_cast<const int32_t*>(dev + plan.entries_off());
+        A.tokens = reinterpret_cast<const int32_t*>(dev + plan.tokens_off());
+        A.pages = reinterpret_cast<const int32_t*>(dev + plan.pages_off());
+        A.n_rows = (int32_t)plan.rows.size();
+        A.n_copies = (int32_t)plan.copies.size();
+        ok = launched(f, launch_kv_take(A, plan.in_place, hs));
+        if (ok != SLORA_OK) (void)hipStreamSynchronize(hs);     // nothing writes pages that are given back
+      }
+      if (ok != SLORA_OK) {
+        pool_untake_pages(kv->pool, kv->d.cls, need, ids.data());
+        return ok;
+      }
+    }
+    // nothing below can fail: first what the new sequences hold, then what the old ones let go of
+    int64_t copy = 0;
+    for (size_t i = 0; i < plan.parts.size(); ++i) {
+      const TakePlan::Part& part = plan.parts[i];
+      for (size_t b = 0; b < part.from.size(); ++b) {
+        if (part.from[b] < 0) {
+          made[i].held[b] = kv->blocks.add(ids.data() + copy++ * per, per);
+        } else {
+          made[i].held[b] = kv->seqs[part.src].held[part.from[b]];
+          ++kv->blocks.refs[made[i].held[b]];
+        }
+      }
+    }
+    for (size_t i = 0; i < plan.parts.size(); ++i) {
+      Seq& s = kv->seqs[plan.parts[i].dst];
+      for (int32_t record : s.held)
+        if (kv->blocks.release(record)) pool_return_pages(kv->pool, kv->d.cls, per, kv->pages_of(record));
+      s = std::move(made[i]);
+    }
+  } catch (const std::bad_alloc&) {
+    return fail(SLORA_E_NOMEM, f + ": out of host memory");
+  }
+  return SLORA_OK;
 }
 
 slora_status slora_kv_read(slora_kv* kv, const slora_kv_step* st, int32_t layer, void* k, int64_t k_stride, void* v,

@@ -49,6 +49,7 @@ EXPORTED = [
     "slora_kv_pages", "slora_kv_build_step", "slora_kv_step_destroy", "slora_kv_step_get_info",
     "slora_kv_step_upload", "slora_kv_append", "slora_kv_attend", "slora_kv_read",
     "slora_kv_append_norm", "slora_kv_rotary_table", "slora_kv_build_step_window", "slora_kv_attend_sinks",
+    "slora_kv_take", "slora_kv_take_bytes", "slora_kv_position",
 ]
 # include/slora_probe.h: bandwidth probes (measurement only)
 EXPORTED_PROBE = ["slora_probe_read", "slora_probe_gather"]
@@ -186,6 +187,11 @@ def lib():
             "slora_kv_attend": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, c_float, c_int32, P, c_size_t, P]),
             "slora_kv_attend_sinks": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, c_float, c_int32, c_int32, P,
                                                 c_size_t, P]),
+            "slora_kv_take": (c_int32, [P, c_int32, POINTER(c_int32), POINTER(c_int32), POINTER(c_int32),
+                                        POINTER(c_int64), P, c_size_t, P]),
+            "slora_kv_take_bytes": (c_size_t, [P, c_int32, POINTER(c_int32), POINTER(c_int32), POINTER(c_int32),
+                                               POINTER(c_int64)]),
+            "slora_kv_position": (c_int64, [P, c_int32]),
             "slora_kv_read": (c_int32, [P, P, c_int32, P, c_int64, P, c_int64, P]),
             "slora_probe_read": (c_int32, [P, c_int64, c_int32, c_int32, P, P, P, P]),
             "slora_probe_gather": (c_int32, [P, c_int64, c_int64, P, c_int64, P, c_int64, c_int64, P,
@@ -577,6 +583,37 @@ def slora_kv_drop(kv, seq: int) -> None:
 
 def slora_kv_length(kv, seq: int) -> int:
     return int(lib().slora_kv_length(kv, seq))
+
+
+def slora_kv_position(kv, seq: int) -> int:
+    return int(lib().slora_kv_position(kv, seq))
+
+
+def _taken(kv, dst, src, ranges):
+    """The arrays of a call of slora_kv_take, and what keeps them alive."""
+    dst, src = (np.ascontiguousarray(x, dtype=np.int32) for x in (dst, src))
+    if dst.ndim != 1 or dst.shape != src.shape or len(ranges) != dst.size:
+        raise ValueError("one source and one list of ranges per sequence")
+    pairs = [np.asarray([(0, max(0, slora_kv_length(kv, int(s))))] if r is None else r, dtype=np.int64).reshape(-1, 2)
+             for s, r in zip(src, ranges)]
+    counts = np.array([len(p) for p in pairs], dtype=np.int32)
+    pairs = np.ascontiguousarray(np.concatenate(pairs)) if pairs else np.zeros((0, 2), np.int64)
+    return (dst.size, _i32p(dst), _i32p(src), _i32p(counts), pairs.ctypes.data_as(POINTER(c_int64))), (dst, src, pairs)
+
+
+def slora_kv_take_bytes(kv, dst, src, ranges) -> int:
+    args, _keep = _taken(kv, dst, src, ranges)
+    n = int(lib().slora_kv_take_bytes(kv, *args))
+    if n == 0:
+        _check(SLORA_E_INVAL, "slora_kv_take_bytes")
+    return n
+
+
+def slora_kv_take(kv, dst, src, ranges, dev_meta=None, dev_meta_bytes: int = 0, stream=None) -> None:
+    """Sequence dst[i] becomes the tokens of src[i] in ranges[i]: (first, last) pairs, or None for all of them."""
+    args, _keep = _taken(kv, dst, src, ranges)
+    dev_meta = _area(dev_meta, dev_meta_bytes, kv.device, "dev_meta")
+    _check(lib().slora_kv_take(kv, *args, dev_meta, int(dev_meta_bytes), _stream(stream)), "slora_kv_take")
 
 
 def slora_kv_pages(kv, seq: int, layer: int = 0, head: int = 0) -> np.ndarray:

@@ -1,11 +1,69 @@
-"""KvCase with attention over a window and the first tokens, for the tests of those."""
+"""KvCase with attention over a window and the first tokens, and with sequences made of others' tokens, in all layers."""
 import numpy as np
 
+from oracle import kv_oracle as O
 from rank_gemm_page_amd import slora as S
 from tests.kv_case import KvCase, half_step
 
 
 class MoreCase(KvCase):
+    def __init__(self, *a, positions=None, **kw):
+        super().__init__(*a, **kw)
+        if positions:
+            self.model.cs = O.angles(positions, self.model.rot)
+            self.cos_sin = self.torch.from_numpy(self.model.cs).to("cuda:0")
+
+    def grow(self, seqs, counts, gain=1.0, attend=None):
+        """A step of drawn rows in every layer; attend: (window, sinks) of the attention that follows, checked."""
+        n = int(sum(counts))
+        st, info, ws = self.step(seqs, counts)
+        starts = [self.model.length(s) for s in seqs]
+        for layer in range(self.n_layers):
+            q, k, v = self.draw(n, self.n_heads), self.draw(n, self.n_kv, gain), self.draw(n, self.n_kv, gain)
+            out = self.torch.zeros((n, self.n_heads, self.dim), dtype=self.tdtype, device="cuda:0")
+            S.slora_kv_append(self.kv, st, layer, self.device(k), self.device(v), self.device(q), out,
+                              cos_sin=self.cos_sin, stream=self.torch.cuda.current_stream())
+            at = 0
+            for s, m in zip(seqs, counts):
+                first = self.model.position(s, layer)
+                self.model.append(s, layer, k[at:at + m], v[at:at + m])
+                self.check_rotated(out[at:at + m], q[at:at + m], first)
+                at += m
+            if attend:
+                got = self.attend_sinks(st, out, ws, self.dim ** -0.5, *attend, layer=layer)
+                self.check_sinks(got, out, seqs, counts, starts, self.dim ** -0.5, *attend, layer=layer)
+        return st
+
+    def take(self, made, stream=None):
+        """made: (dst, src, ranges) of each."""
+        args = [[m[i] for m in made] for i in range(3)]
+        n = S.slora_kv_take_bytes(self.kv, *args)
+        meta = self.torch.full((n,), 255, dtype=self.torch.uint8, device="cuda:0")
+        self.metas.append(meta)
+        S.slora_kv_take(self.kv, *args, meta, n, stream or self.torch.cuda.current_stream())
+        self.model.take([(d, s, [(0, self.model.length(s))] if r is None else r) for d, s, r in made])
+        for d, _, _ in made:
+            assert S.slora_kv_length(self.kv, d) == self.model.length(d)
+            assert S.slora_kv_position(self.kv, d) == self.model.position(d)
+
+    def drop(self, seq):
+        S.slora_kv_drop(self.kv, seq)
+        self.model.drop(seq)
+
+    def pages(self, seq):
+        """[block, layer, head] page ids."""
+        return np.stack([[S.slora_kv_pages(self.kv, seq, layer, h) for h in range(self.n_kv)]
+                         for layer in range(self.n_layers)]).transpose(2, 0, 1)
+
+    def free(self):
+        return S.slora_free_count(self.pool, 0)
+
+    def check_all(self, seqs):
+        """What every sequence holds, in every layer."""
+        seqs = [s for s in seqs if self.model.length(s)]
+        for layer in range(self.n_layers if seqs else 0):
+            self.check_read(seqs, layer)
+
     def step(self, seqs, counts, reread=False, stream=None, **cut):
         if not cut:
             return super().step(seqs, counts, reread, stream)
