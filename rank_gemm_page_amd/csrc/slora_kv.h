@@ -63,7 +63,7 @@ struct KvAppend {
   // the norms of q and k, where they have any: weights (NULL: ones) of all heads,
   // or those of head h at h * w_stride
   const void* q_weight; const void* k_weight;
-  float eps;
+  float eps, w_mean;          // w_mean: 1 / head_dim
   int32_t w_stride;           // 0 or head_dim
 };
 
@@ -94,7 +94,7 @@ struct KvRotary {
   double amplitude;
   float* out;                 // [n][2 * half]
   int64_t first, n;
-  int32_t half, run;          // run: positions of a thread
+  int32_t half, bases;        // bases: of a workgroup (set by the launch)
 };
 
 // Sequences made of others' tokens.  The page table rows of sequence dst from block `first` on: n entries, of which

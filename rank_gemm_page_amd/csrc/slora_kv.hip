@@ -93,9 +93,10 @@ __device__ __forceinline__ double wave_sum(double v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
-__device__ __forceinline__ double root(double sum, const KvAppend& A) { return rsqrt(sum / A.kv.dim + (double)A.eps); }
+// (1 / dim is a power of two)
+__device__ __forceinline__ double root(double sum, const KvAppend& A) { return rsqrt(sum * A.w_mean + (double)A.eps); }
 __device__ __forceinline__ float root(float sum, const KvAppend& A) {
-  return 1.f / sqrtf(sum / (float)A.kv.dim + A.eps);
+  return __builtin_amdgcn_rsqf(__builtin_fmaf(sum, A.w_mean, A.eps));
 }
 template <typename T>
 __device__ __forceinline__ const T* weights_of(const void* w, int32_t stride, int head) {
@@ -263,6 +264,11 @@ __device__ __forceinline__ void store_one(const KvAppend& A, uint32_t at, int la
     }
 }
 
+// A unit of keys between the passes: as it was loaded, or, normed, with its pairs
+// turned (made again from what was loaded it took 8 us more of 32 prompts).
+template <typename T, bool NORM> struct Kept { Pairs<T> x; Turn t; };
+template <typename T> struct Kept<T, true> { double a[8], b[8]; };
+
 template <typename T, int CODE, bool NORM>
 __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int tid, uint32_t* lds) {
   using C = Code<CODE>;
@@ -288,38 +294,51 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
     *t = load_turn(kv, A.cos_sin, it.pos0 + slot, c);
   };
   // (a head's lanes are in a loop together: units are whole heads)
-  auto rms = [&](const Pairs<T>& x) { return NORM ? root(head_sum(square_sum<double>(x), ush), A) : 1.; };
-  auto turn = [&](const Pairs<T>& x, const Turn& t, double r, int j, double* ra, double* rb) {
-    if (NORM) turned((double)x.a[j] * r * (double)w.a[j], (double)x.b[j] * r * (double)w.b[j], t.c[j], t.s[j], ra, rb);
-    else turned((double)x.a[j], (double)x.b[j], t.c[j], t.s[j], ra, rb);
+  auto made = [&](int u) {
+    Pairs<T> x;
+    Turn t;
+    load(u, &x, &t);
+    Kept<T, NORM> k;
+    if constexpr (NORM) {
+      const double r = root(head_sum(square_sum<double>(x), ush), A);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        turned((double)x.a[j] * (double)w.a[j] * r, (double)x.b[j] * (double)w.b[j] * r, t.c[j], t.s[j], &k.a[j],
+               &k.b[j]);
+    } else {
+      k.x = x;
+      k.t = t;
+    }
+    return k;
   };
-  auto largest = [&](const Pairs<T>& x, const Turn& t, double r) {
+  auto turn = [&](const Kept<T, NORM>& k, int j, double* ra, double* rb) {
+    if constexpr (NORM) {
+      *ra = k.a[j];
+      *rb = k.b[j];
+    } else {
+      turned((double)k.x.a[j], (double)k.x.b[j], k.t.c[j], k.t.s[j], ra, rb);
+    }
+  };
+  auto largest = [&](const Kept<T, NORM>& k) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       double ra, rb;
-      turn(x, t, r, j, &ra, &rb);
+      turn(k, j, &ra, &rb);
       m = max(m, max(magnitude(ra), magnitude(rb)));
     }
     return m;
   };
-  Pairs<T> kept{};
-  Turn kept_turn{};
-  if (tid < units) load(tid, &kept, &kept_turn);
-  const double kept_rms = rms(kept);
-  uint32_t m = tid < units || !NORM ? largest(kept, kept_turn, kept_rms) : 0;
-  for (int u = tid + kThreads; u < units; u += kThreads) {
-    Pairs<T> x;
-    Turn t;
-    load(u, &x, &t);
-    m = max(m, largest(x, t, rms(x)));
-  }
+  Kept<T, NORM> kept{};
+  if (tid < units) kept = made(tid);
+  uint32_t m = largest(kept);
+  for (int u = tid + kThreads; u < units; u += kThreads) m = max(m, largest(made(u)));
   m = max(team_max(m, lds), held);
   const bool bad = m >= 0x7F800000u;
   if (tid == 0) it.range[0] = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m);
   const double grown = __uint_as_float(m), inv = m ? (double)C::kTop / grown : 0.;
 
-  auto put = [&](int u, const Pairs<T>& x, const Turn& t, double r) {
+  auto put = [&](int u, const Kept<T, NORM>& k) {
     const int slot = blk.slot0 + (u >> ush), c = u & ((1 << ush) - 1);
     int a, b;
     unit_runs(kv, c, &a, &b);
@@ -327,7 +346,7 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       double ra, rb;
-      turn(x, t, r, j, &ra, &rb);
+      turn(k, j, &ra, &rb);
       wa[j >> 2] |= C::nearest(ra * inv) << (8 * (j & 3));
       wb[j >> 2] |= C::nearest(rb * inv) << (8 * (j & 3));
     }
@@ -342,13 +361,8 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
     *reinterpret_cast<uint2*>(it.page + kv_k_byte(slot, a, it.dim)) = first;
     *reinterpret_cast<uint2*>(it.page + kv_k_byte(slot, b, it.dim)) = second;
   };
-  if (tid < units) put(tid, kept, kept_turn, kept_rms);
-  for (int u = tid + kThreads; u < units; u += kThreads) {
-    Pairs<T> x;
-    Turn t;
-    load(u, &x, &t);
-    put(u, x, t, rms(x));
-  }
+  if (tid < units) put(tid, kept);
+  for (int u = tid + kThreads; u < units; u += kThreads) put(u, made(u));
   if (blk.slot0 && m != held) {                                // the range grew: older keys are coded again
     const double ratio = bad ? 0. : (double)__uint_as_float(held) / grown;
     for (int u = tid; u < blk.slot0 << ush; u += kThreads) {
@@ -483,38 +497,53 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
   const T* in = (const T*)A.q + row * A.q_stride;
   T* out = (T*)A.q_out + row * A.q_out_stride;
   const int h1 = min(kv.n_heads, h0 + A.q_heads);
+  // NORM: four heads' elements are loaded before the first sum over lanes (loops
+  // that hold one are not unrolled by the compiler)
   typedef typename Norm<T>::type W;
+  constexpr int N = NORM && sizeof(T) == 2 ? 4 : 1;
   constexpr int kHeads = NORM ? 1 : 4;
   Pairs<T> w;
   if (NORM && !A.w_stride) w = load_weights<T>(A, A.q_weight, 0, a, b);
 #pragma unroll kHeads
-  for (int h = h0; h < h1; ++h) {
-    Pairs<T> x = load_pairs(kv, in + h * kv.dim, a, b);
-    W r = 1;
-    if (NORM) {
-      if (A.w_stride) w = load_weights<T>(A, A.q_weight, h, a, b);
-      r = root(head_sum(square_sum<W>(x), ush), A);
-    }
-    if (NORM || turns) {
+  for (int hh = h0; hh < h1; hh += N) {
+    Pairs<T> xs[N];
+    W r[N];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float xa = (float)x.a[j], xb = (float)x.b[j], ra, rb;
-        if (NORM) {
-          ra = xa = (float)((W)x.a[j] * r * (W)w.a[j]);
-          rb = xb = (float)((W)x.b[j] * r * (W)w.b[j]);
+    for (int n = 0; n < N; ++n) {
+      xs[n] = load_pairs(kv, in + (NORM ? min(hh + n, h1 - 1) : hh) * kv.dim, a, b);
+      r[n] = 1;
+    }
+    if (NORM) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) r[n] = root(head_sum(square_sum<W>(xs[n]), ush), A);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int h = hh + n;
+      if (NORM && h >= h1) break;
+      Pairs<T> x = xs[n];
+      if (NORM && A.w_stride) w = load_weights<T>(A, A.q_weight, h, a, b);
+      if (NORM || turns) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float xa = (float)x.a[j], xb = (float)x.b[j], ra, rb;
+          if (NORM) {
+            ra = xa = (float)((W)x.a[j] * r[n] * (W)w.a[j]);
+            rb = xb = (float)((W)x.b[j] * r[n] * (W)w.b[j]);
+          }
+          if (!NORM || turns) turned(xa, xb, t.c[j], t.s[j], &ra, &rb);
+          x.a[j] = (T)ra;
+          x.b[j] = (T)rb;
         }
-        if (!NORM || turns) turned(xa, xb, t.c[j], t.s[j], &ra, &rb);
-        x.a[j] = (T)ra;
-        x.b[j] = (T)rb;
       }
+      V8 first = x.a, second = x.b;
+      if (kv.pairs == SLORA_KV_NEIGHBOURS) {
+        first = __builtin_shufflevector(x.a, x.b, 0, 8, 1, 9, 2, 10, 3, 11);
+        second = __builtin_shufflevector(x.a, x.b, 4, 12, 5, 13, 6, 14, 7, 15);
+      }
+      *reinterpret_cast<V8*>(out + h * kv.dim + a) = first;
+      *reinterpret_cast<V8*>(out + h * kv.dim + b) = second;
     }
-    V8 first = x.a, second = x.b;
-    if (kv.pairs == SLORA_KV_NEIGHBOURS) {
-      first = __builtin_shufflevector(x.a, x.b, 0, 8, 1, 9, 2, 10, 3, 11);
-      second = __builtin_shufflevector(x.a, x.b, 4, 12, 5, 13, 6, 14, 7, 15);
-    }
-    *reinterpret_cast<V8*>(out + h * kv.dim + a) = first;
-    *reinterpret_cast<V8*>(out + h * kv.dim + b) = second;
   }
 }
 

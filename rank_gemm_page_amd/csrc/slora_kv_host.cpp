@@ -375,6 +375,7 @@ slora_status append(const std::string& f, slora_kv* kv, const slora_kv_step* st,
     A.q_weight = norm->q_weight;
     A.k_weight = norm->k_weight;
     A.eps = norm->eps;
+    A.w_mean = 1.f / (float)kv->d.head_dim;
     A.w_stride = norm->per_head ? kv->d.head_dim : 0;
   }
   ok = launched(f, launch_kv_append(A, norm != nullptr, static_cast<hipStream_t>(stream)));
@@ -858,8 +859,11 @@ slora_status slora_kv_rotary_table(slora_kv* kv, const slora_kv_rotary* r, int64
   if (r->scaling == SLORA_KV_ROT_BASE) log_base += std::log(factor) * rot / (rot - 2);
   auto pair_of = [&](double turns) { return rot * std::log((wide)r->trained / (pi2 * turns)) / (2 * log_base); };
   KvRotary R{};
+  wide by16[8], by1[16];                                       // t_i = by16[i / 16] by1[i % 16]
+  for (int32_t i = 0; i < 16; ++i) by1[i] = std::exp(-2 * i * log_base / rot);
+  for (int32_t i = 0; i < 8; ++i) by16[i] = std::exp(-32 * i * log_base / rot);
   for (int32_t i = 0; i < rot / 2; ++i) {
-    wide t = std::exp(-2 * i * log_base / rot), keep = 1.L;
+    wide t = by16[i / 16] * by1[i % 16], keep = 1.L;
     if (r->scaling == SLORA_KV_ROT_LINEAR) keep = 0.L;
     if (r->scaling == SLORA_KV_ROT_BANDS)
       keep = (r->trained * t / pi2 - r->low) / ((wide)r->high - r->low);
