@@ -204,6 +204,7 @@ hipError_t launch_forward(const ForwardLaunch& F, hipStream_t stream, hipEvent_t
 
 // Zero n_words 32-bit words at p (a fill kernel; no memset node in the stream).
 hipError_t launch_zero_words(void* p, int64_t n_words, hipStream_t stream);
+hipError_t launch_fetch_words(void* to, const void* pinned, int64_t n_words, hipStream_t stream);
 
 // Adapter images staged on the device for one scatter launch.  Image i sits
 // at stage + img_off[i]: n_proj x rank[i] A^T rows of a_row_bytes, then as many

@@ -1067,6 +1067,24 @@ hipError_t launch_zero_words(void* p, int64_t n_words, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Pinned host memory read by a kernel: 16 bytes a thread, the last ones word by word.
+__global__ __launch_bounds__(kThreads) void fetch_words_kernel(uint32_t* to, const uint32_t* from, int64_t n) {
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (i + 4 <= n) {
+    *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(from + i);
+  } else {
+    for (int64_t j = i; j < n; ++j) to[j] = from[j];
+  }
+}
+
+hipError_t launch_fetch_words(void* to, const void* pinned, int64_t n_words, hipStream_t stream) {
+  if (n_words <= 0) return hipSuccess;
+  const int64_t blocks = (n_words + 4 * kThreads - 1) / (4 * kThreads);
+  fetch_words_kernel<<<dim3((unsigned)blocks), dim3(kThreads), 0, stream>>>(
+      static_cast<uint32_t*>(to), static_cast<const uint32_t*>(pinned), n_words);
+  return hipGetLastError();
+}
+
 // ---------------------------------------------------------------------------
 // Adapter fetch, second half: the images are already in device staging (one
 // copy-engine transfer each); one workgroup per row moves the row into its

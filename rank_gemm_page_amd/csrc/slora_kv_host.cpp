@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <numeric>
 #include <string>
 #include <vector>
 
@@ -463,14 +464,22 @@ const char* plan_take(const slora_kv* kv, int32_t n, const int32_t* dst, const i
   const int32_t bt = kv->block, layers = kv->d.n_layers;
   int64_t at = 0;
   std::vector<std::pair<int64_t, int64_t>> kept;               // ranges, those that touch joined
+  std::vector<int32_t> ready;                                  // [block] tokens of the source in every layer
   for (int32_t i = 0; i < n; ++i) {
     const bool same = dst[i] == src[i];
     if (!same && changed[src[i]]) return "the source of a sequence is changed by the same call";
     const Seq& s = kv->seqs[src[i]];
     if (!same && kv->seqs[dst[i]].blocks) return "a sequence that is made from another one must be empty";
+    if (i == 0 || src[i] != src[i - 1]) {
+      ready.resize((size_t)s.entered);
+      for (int32_t b = 0; b < s.entered; ++b)
+        ready[b] = *std::min_element(s.stored.begin() + (size_t)b * layers, s.stored.begin() + (size_t)(b + 1) * layers);
+    }
     kept.clear();
-    int64_t end = 0;
+    int64_t end = 0, b = 0;                                    // b: block of the range's first token
     TakePlan::Part part;
+    part.runs.reserve((size_t)n_ranges[i]);
+    kept.reserve((size_t)n_ranges[i]);
     part.dst = dst[i];
     part.src = src[i];
     for (int32_t r = 0; r < n_ranges[i]; ++r, ++at) {
@@ -478,11 +487,11 @@ const char* plan_take(const slora_kv* kv, int32_t n, const int32_t* dst, const i
       if (lo < end || hi < lo || hi > s.len) return "ranges must ascend within the sequence's tokens";
       end = hi;
       if (lo == hi) continue;
-      for (int64_t b = lo / bt; b * bt < hi; ++b) {
+      while ((b + 1) * bt <= lo) ++b;
+      for (;; ++b) {
         if (b >= s.entered) return "the step of a token has not been uploaded";
-        for (int32_t layer = 0; layer < layers; ++layer)
-          if (s.stored[(size_t)b * layers + layer] < std::min<int64_t>(bt, hi - b * bt))
-            return "a token has not been appended in every layer";
+        if (ready[b] < std::min<int64_t>(bt, hi - b * bt)) return "a token has not been appended in every layer";
+        if ((b + 1) * bt >= hi) break;
       }
       if (!kept.empty() && kept.back().second == lo) kept.back().second = hi;
       else kept.push_back({lo, hi});
@@ -505,6 +514,7 @@ const char* plan_take(const slora_kv* kv, int32_t n, const int32_t* dst, const i
     // blocks
     size_t k = 0;
     int64_t p = kept.empty() ? 0 : kept[0].first;
+    part.from.reserve((size_t)((part.len + bt - 1) / bt));
     for (int64_t left = part.len; left > 0;) {
       const int64_t count = std::min<int64_t>(bt, left), block = p / bt;
       left -= count;
@@ -518,7 +528,8 @@ const char* plan_take(const slora_kv* kv, int32_t n, const int32_t* dst, const i
         if (same) plan->in_place = true;
         for (int64_t want = count; want > 0;) {
           const int64_t take = std::min(want, kept[k].second - p);
-          for (int64_t t = 0; t < take; ++t) plan->tokens.push_back((int32_t)(p + t));
+          plan->tokens.resize(plan->tokens.size() + (size_t)take);
+          std::iota(plan->tokens.end() - take, plan->tokens.end(), (int32_t)p);
           want -= take;
           p += take;
           if (p == kept[k].second && want > 0) p = kept[++k].first;

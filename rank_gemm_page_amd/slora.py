@@ -594,10 +594,13 @@ def _taken(kv, dst, src, ranges):
     dst, src = (np.ascontiguousarray(x, dtype=np.int32) for x in (dst, src))
     if dst.ndim != 1 or dst.shape != src.shape or len(ranges) != dst.size:
         raise ValueError("one source and one list of ranges per sequence")
-    pairs = [np.asarray([(0, max(0, slora_kv_length(kv, int(s))))] if r is None else r, dtype=np.int64).reshape(-1, 2)
-             for s, r in zip(src, ranges)]
-    counts = np.array([len(p) for p in pairs], dtype=np.int32)
-    pairs = np.ascontiguousarray(np.concatenate(pairs)) if pairs else np.zeros((0, 2), np.int64)
+    if any(r is None for r in ranges):
+        ranges = [[(0, max(0, slora_kv_length(kv, int(s))))] if r is None else r for s, r in zip(src, ranges)]
+    counts = np.array([len(r) for r in ranges], dtype=np.int32)
+    pairs = [r for r in ranges if len(r)] or [np.zeros((0, 2))]
+    pairs = np.ascontiguousarray(np.concatenate(pairs), dtype=np.int64)
+    if pairs.ndim != 2 or pairs.shape[1] != 2:
+        raise ValueError("ranges are (first, last) pairs")
     return (dst.size, _i32p(dst), _i32p(src), _i32p(counts), pairs.ctypes.data_as(POINTER(c_int64))), (dst, src, pairs)
 
 
