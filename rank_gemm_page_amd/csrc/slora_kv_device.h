@@ -92,15 +92,37 @@ __device__ __forceinline__ const int32_t* kv_row(const KvView& kv, int seq, int 
 }
 
 // ---------------------------------------------------------------------------
-// Codes of a range that grew: nearest(code * (old range / new range)).
+// Codes of a range that grew: nearest(code * (old range / new range)).  The ratio
+// is at most 1, so that no code passes the last one.
+
+template <int CODE> struct Again;
+
+// (byte - 128) * ratio as one fma, whose product with 128 is exact
+template <> struct Again<SLORA_KV_INT8> {
+  static __device__ __forceinline__ uint32_t one(uint32_t byte, double ratio) {
+#pragma clang fp contract(off)
+    return (uint32_t)__double2loint(__builtin_fma((double)(float)byte, ratio, -128. * ratio) + (0x1.8p52 + 128.));
+  }
+  static __device__ __forceinline__ uint32_t four(uint32_t old, double r0, double r1, double r2, double r3) {
+    const uint32_t a = one(old & 0xFF, r0), b = one((old >> 8) & 0xFF, r1), c = one((old >> 16) & 0xFF, r2);
+    const uint32_t low = __builtin_amdgcn_perm(b, a, 0x0c0c0400u);
+    return low | __builtin_amdgcn_perm(one(old >> 24, r3), c, 0x04000c0cu);
+  }
+};
+
+template <> struct Again<SLORA_KV_FP8> {
+  static __device__ __forceinline__ uint32_t four(uint32_t old, double r0, double r1, double r2, double r3) {
+    const auto low = __builtin_amdgcn_cvt_pk_f32_fp8((int)old, false);
+    const auto high = __builtin_amdgcn_cvt_pk_f32_fp8((int)old, true);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32((float)((double)low[0] * r0), (float)((double)low[1] * r1), 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32((float)((double)high[0] * r2), (float)((double)high[1] * r3), w, true);
+    return (uint32_t)w;
+  }
+};
 
 template <int CODE>
 __device__ __forceinline__ uint32_t again4(uint32_t old, double ratio) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w |= Code<CODE>::nearest((double)Code<CODE>::value((old >> (8 * j)) & 0xFF) * ratio) << (8 * j);
-  return w;
+  return Again<CODE>::four(old, ratio, ratio, ratio, ratio);
 }
 template <int CODE>
 __device__ __forceinline__ uint4 again16(uint4 o, double ratio) {
