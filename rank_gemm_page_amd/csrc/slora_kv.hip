@@ -138,6 +138,23 @@ __device__ __forceinline__ W square_sum(const Pairs<T>& x) {
 __device__ __forceinline__ uint32_t magnitude(double x) { return __float_as_uint(fabsf((float)x)); }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(fabsf(x)); }
 
+// The largest magnitude of eight elements; fp16 bit patterns order as the fp32
+// ones do, two at a time.
+__device__ __forceinline__ uint32_t largest8(float8v x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) m = max(m, magnitude(x[n]));
+  return m;
+}
+__device__ __forceinline__ uint32_t largest8(half8 x) {
+  typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+  const uint4v w = __builtin_bit_cast(uint4v, x) & 0x7FFF7FFFu;
+  ushort2v m = __builtin_bit_cast(ushort2v, w[0]);
+#pragma unroll
+  for (int n = 1; n < 4; ++n) m = __builtin_elementwise_max(m, __builtin_bit_cast(ushort2v, w[n]));
+  return magnitude((float)__builtin_bit_cast(_Float16, (uint16_t)max(m[0], m[1])));
+}
+
 // Elements of a value unit as they are read: 8 of each of two tokens.  old: the
 // unit as the page holds it, where the append leaves some of its tokens as they
 // are.
@@ -301,9 +318,11 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
     Kept<T, NORM> k;
     if constexpr (NORM) {
       const double r = root(head_sum(square_sum<double>(x), ush), A);
+      Pairs<T> y = w;
+      asm volatile("" : "+v"(y.a), "+v"(y.b));                 // else the weights stay beside it in 64 bits
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        turned((double)x.a[j] * (double)w.a[j] * r, (double)x.b[j] * (double)w.b[j] * r, t.c[j], t.s[j], &k.a[j],
+        turned((double)x.a[j] * (double)y.a[j] * r, (double)x.b[j] * (double)y.b[j] * r, t.c[j], t.s[j], &k.a[j],
                &k.b[j]);
     } else {
       k.x = x;
@@ -342,13 +361,14 @@ __device__ __forceinline__ void store_keys(const KvAppend& A, uint32_t at, int t
     const int slot = blk.slot0 + (u >> ush), c = u & ((1 << ush) - 1);
     int a, b;
     unit_runs(kv, c, &a, &b);
-    uint32_t wa[2] = {0, 0}, wb[2] = {0, 0};
+    uint32_t wa[2], wb[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      double ra, rb;
-      turn(k, j, &ra, &rb);
-      wa[j >> 2] |= C::nearest(ra * inv) << (8 * (j & 3));
-      wb[j >> 2] |= C::nearest(rb * inv) << (8 * (j & 3));
+    for (int h = 0; h < 2; ++h) {
+      double ra[4], rb[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) turn(k, 4 * h + j, &ra[j], &rb[j]);
+      wa[h] = C::four(ra[0] * inv, ra[1] * inv, ra[2] * inv, ra[3] * inv);
+      wb[h] = C::four(rb[0] * inv, rb[1] * inv, rb[2] * inv, rb[3] * inv);
     }
     uint2 first = make_uint2(wa[0], wa[1]), second = make_uint2(wb[0], wb[1]);
     if (kv.pairs == SLORA_KV_NEIGHBOURS) {
@@ -400,12 +420,7 @@ __device__ __forceinline__ void store_values(const KvAppend& A, uint32_t at, int
         x->x[h] = *reinterpret_cast<const V8*>(in + (it.row0 + slot) * A.v_stride + e * 32);
     }
   };
-  auto largest = [&](const Values<T>& x) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int n = 0; n < 16; ++n) m = max(m, magnitude((float)x.x[n >> 3][n & 7]));
-    return m;
-  };
+  auto largest = [&](const Values<T>& x) { return max(largest8(x.x[0]), largest8(x.x[1])); };
   Values<T> kept{};
   if (tid < units) load(tid, &kept);
   uint32_t m = largest(kept);
@@ -432,9 +447,10 @@ __device__ __forceinline__ void store_values(const KvAppend& A, uint32_t at, int
       }
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
-        uint32_t c = 0;
+        double y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c |= C::nearest((double)(float)x.x[h][2 * j + d] * inv) << (8 * j);
+        for (int j = 0; j < 4; ++j) y[j] = (double)(float)x.x[h][2 * j + d] * inv;
+        const uint32_t c = C::four(y[0], y[1], y[2], y[3]);
         w[2 * d + h] = quad_transpose(bad ? C::kZero * 0x01010101u : c, lane);
       }
     }

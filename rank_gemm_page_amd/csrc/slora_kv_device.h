@@ -22,6 +22,7 @@ __device__ __forceinline__ uint4 ld16_once(const void* p) {
 // it is the fp16 number 1024 + c + 128, so two codes become fp16 with one byte
 // permute and one packed subtraction.  An e4m3 code is its byte.
 
+// nearest: the code of a value in units of a code; four: of four, a byte each.
 template <int CODE> struct Code;
 
 template <> struct Code<SLORA_KV_INT8> {
@@ -52,6 +53,10 @@ template <> struct Code<SLORA_KV_INT8> {
 #pragma clang fp contract(off)
     return (uint32_t)min(max(__double2loint(x + (0x1.8p52 + 128.)), 1), 255);
   }
+  static __device__ __forceinline__ uint32_t four(double a, double b, double c, double d) {
+    return __builtin_amdgcn_perm(nearest(b), nearest(a), 0x0c0c0400u) |
+           __builtin_amdgcn_perm(nearest(d), nearest(c), 0x04000c0cu);
+  }
 };
 
 template <> struct Code<SLORA_KV_FP8> {
@@ -70,8 +75,12 @@ template <> struct Code<SLORA_KV_FP8> {
   // The definition rounds the 64-bit product to fp32 and then to e4m3.  A
   // subnormal range's values are held at the last code as above.
   static __device__ __forceinline__ uint32_t nearest(double x) {
-    const float y = __builtin_amdgcn_fmed3f((float)x, -kTop, kTop);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, 0.f, 0, false) & 0xFF;
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(held(x), 0.f, 0, false) & 0xFF;
+  }
+  static __device__ __forceinline__ float held(double x) { return __builtin_amdgcn_fmed3f((float)x, -kTop, kTop); }
+  static __device__ __forceinline__ uint32_t four(double a, double b, double c, double d) {
+    const int low = __builtin_amdgcn_cvt_pk_fp8_f32(held(a), held(b), 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(held(c), held(d), low, true);
   }
 };
 
