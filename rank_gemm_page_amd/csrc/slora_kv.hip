@@ -149,9 +149,12 @@ __device__ __forceinline__ uint32_t largest8(float8v x) {
 __device__ __forceinline__ uint32_t largest8(half8 x) {
   typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
   const uint4v w = __builtin_bit_cast(uint4v, x) & 0x7FFF7FFFu;
-  ushort2v m = __builtin_bit_cast(ushort2v, w[0]);
+  ushort2v m = {0, 0};
 #pragma unroll
-  for (int n = 1; n < 4; ++n) m = __builtin_elementwise_max(m, __builtin_bit_cast(ushort2v, w[n]));
+  for (int n = 0; n < 4; ++n) {
+    const uint32_t two = w[n];                                 // (a bit cast of w[n] itself takes w[0])
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(ushort2v, two));
+  }
   return magnitude((float)__builtin_bit_cast(_Float16, (uint16_t)max(m[0], m[1])));
 }
 
