@@ -516,52 +516,59 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
   const T* in = (const T*)A.q + row * A.q_stride;
   T* out = (T*)A.q_out + row * A.q_out_stride;
   const int h1 = min(kv.n_heads, h0 + A.q_heads);
-  // NORM: four heads' elements are loaded before the first sum over lanes (loops
-  // that hold one are not unrolled by the compiler)
-  typedef typename Norm<T>::type W;
-  constexpr int N = NORM && sizeof(T) == 2 ? 4 : 1;
-  constexpr int kHeads = NORM ? 1 : 4;
-  Pairs<T> w;
-  if (NORM && !A.w_stride) w = load_weights<T>(A, A.q_weight, 0, a, b);
-#pragma unroll kHeads
-  for (int hh = h0; hh < h1; hh += N) {
-    Pairs<T> xs[N];
-    W r[N];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      xs[n] = load_pairs(kv, in + (NORM ? min(hh + n, h1 - 1) : hh) * kv.dim, a, b);
-      r[n] = 1;
+  auto put = [&](int h, const Pairs<T>& x) {
+    V8 first = x.a, second = x.b;
+    if (kv.pairs == SLORA_KV_NEIGHBOURS) {
+      first = __builtin_shufflevector(x.a, x.b, 0, 8, 1, 9, 2, 10, 3, 11);
+      second = __builtin_shufflevector(x.a, x.b, 4, 12, 5, 13, 6, 14, 7, 15);
     }
-    if (NORM) {
-#pragma unroll
-      for (int n = 0; n < N; ++n) r[n] = root(head_sum(square_sum<W>(xs[n]), ush), A);
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int h = hh + n;
-      if (NORM && h >= h1) break;
-      Pairs<T> x = xs[n];
-      if (NORM && A.w_stride) w = load_weights<T>(A, A.q_weight, h, a, b);
-      if (NORM || turns) {
+    *reinterpret_cast<V8*>(out + h * kv.dim + a) = first;
+    *reinterpret_cast<V8*>(out + h * kv.dim + b) = second;
+  };
+  if constexpr (!NORM) {
+#pragma unroll 4
+    for (int h = h0; h < h1; ++h) {
+      Pairs<T> x = load_pairs(kv, in + h * kv.dim, a, b);
+      if (turns) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float xa = (float)x.a[j], xb = (float)x.b[j], ra, rb;
-          if (NORM) {
-            ra = xa = (float)((W)x.a[j] * r[n] * (W)w.a[j]);
-            rb = xb = (float)((W)x.b[j] * r[n] * (W)w.b[j]);
-          }
-          if (!NORM || turns) turned(xa, xb, t.c[j], t.s[j], &ra, &rb);
+          float ra, rb;
+          turned((float)x.a[j], (float)x.b[j], t.c[j], t.s[j], &ra, &rb);
           x.a[j] = (T)ra;
           x.b[j] = (T)rb;
         }
       }
-      V8 first = x.a, second = x.b;
-      if (kv.pairs == SLORA_KV_NEIGHBOURS) {
-        first = __builtin_shufflevector(x.a, x.b, 0, 8, 1, 9, 2, 10, 3, 11);
-        second = __builtin_shufflevector(x.a, x.b, 4, 12, 5, 13, 6, 14, 7, 15);
+      put(h, x);
+    }
+  } else {
+    // four heads' elements (fp32, whose sums take twice the registers: one's) are
+    // loaded before the first sum over lanes; the compiler unrolls no loop with one
+    typedef typename Norm<T>::type W;
+    constexpr int N = sizeof(T) == 2 ? 4 : 1;
+    Pairs<T> w;
+    if (!A.w_stride) w = load_weights<T>(A, A.q_weight, 0, a, b);
+    for (int hh = h0; hh < h1; hh += N) {
+      Pairs<T> xs[N];
+      W r[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) xs[n] = load_pairs(kv, in + min(hh + n, h1 - 1) * kv.dim, a, b);
+#pragma unroll
+      for (int n = 0; n < N; ++n) r[n] = root(head_sum(square_sum<W>(xs[n]), ush), A);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (hh + n >= h1) break;
+        Pairs<T> x = xs[n];
+        if (A.w_stride) w = load_weights<T>(A, A.q_weight, hh + n, a, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float xa = (float)((W)x.a[j] * r[n] * (W)w.a[j]), xb = (float)((W)x.b[j] * r[n] * (W)w.b[j]);
+          float ra = xa, rb = xb;
+          if (turns) turned(xa, xb, t.c[j], t.s[j], &ra, &rb);
+          x.a[j] = (T)ra;
+          x.b[j] = (T)rb;
+        }
+        put(hh + n, x);
       }
-      *reinterpret_cast<V8*>(out + h * kv.dim + a) = first;
-      *reinterpret_cast<V8*>(out + h * kv.dim + b) = second;
     }
   }
 }
