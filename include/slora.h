@@ -530,7 +530,8 @@ const char* slora_last_error(void);
  * captured into a HIP graph; uploads may not.  A captured append counts as
  * launched when it is captured; its replays are not seen, and keep to the same
  * rule: not after a later step's append to the same blocks, nor after a sequence
- * of the step was dropped. */
+ * of the step was dropped or changed by slora_kv_take, nor an append's after one of
+ * its blocks came to be shared. */
 typedef struct slora_kv slora_kv;
 typedef struct slora_kv_step slora_kv_step;
 
@@ -736,11 +737,12 @@ slora_status slora_kv_attend_sinks(slora_kv* kv, const slora_kv_step* step, int3
  * src[i] shares that block's pages: it takes no memory and no time, and the pages
  * are freed with the last sequence that holds them.  (So ranges that begin and
  * end at multiples of block_tokens move nothing.)  In place, a last block that
- * only lost its end keeps its pages too.  All other blocks are written to pages of their own, taken from the
- * pool for every layer and kv head, all or nothing (SLORA_E_NOMEM): the range of such a block is the
- * largest of the ranges of the blocks that its tokens come from (of keys and of
- * values; NaN where one is), and codes of smaller ones are coded again, as where
- * an append raises a range.
+ * only lost its end keeps its pages too.  All other blocks are written to pages of
+ * their own, taken from the pool for every layer and kv head, all or nothing
+ * (SLORA_E_NOMEM; what is dropped is freed only afterwards): the range of such a
+ * block is the largest of the ranges of the blocks that its tokens come from (of
+ * keys and of values; NaN where one is), and codes of smaller ones are coded again,
+ * as where an append raises a range.
  *
  * Tokens are renumbered 0, 1, ..., for windows, sinks and everything else
  * but the rotation: a token keeps the position that it was rotated by, and the

@@ -597,10 +597,10 @@ def _taken(kv, dst, src, ranges):
     if any(r is None for r in ranges):
         ranges = [[(0, max(0, slora_kv_length(kv, int(s))))] if r is None else r for s, r in zip(src, ranges)]
     counts = np.array([len(r) for r in ranges], dtype=np.int32)
-    pairs = [r for r in ranges if len(r)] or [np.zeros((0, 2))]
-    pairs = np.ascontiguousarray(np.concatenate(pairs), dtype=np.int64)
-    if pairs.ndim != 2 or pairs.shape[1] != 2:
-        raise ValueError("ranges are (first, last) pairs")
+    pairs = np.concatenate([r for r in ranges if len(r)] or [np.zeros((0, 2), np.int64)])
+    if pairs.ndim != 2 or pairs.shape[1] != 2 or pairs.dtype.kind not in "iu":
+        raise ValueError("ranges are (first, last) pairs of whole numbers")
+    pairs = np.ascontiguousarray(pairs, dtype=np.int64)
     return (dst.size, _i32p(dst), _i32p(src), _i32p(counts), pairs.ctypes.data_as(POINTER(c_int64))), (dst, src, pairs)
 
 

@@ -256,6 +256,76 @@ def test_fp32_subnormal_ranges():
         c.check_all([0, 1, 2])
 
 
+@pytest.mark.parametrize("dim,tokens", [(128, 224), (64, 448), (256, 96)])
+@pytest.mark.parametrize("code", CODES)
+def test_blocks_of_more_tokens_than_a_workgroup(dim, tokens, code):
+    """A pool of two classes with the blocks in the larger pages, whose tokens are found some at a time."""
+    n = 80
+    mem = [torch.full((n, 1024), 255, dtype=torch.uint8, device="cuda:0"),
+           torch.full((n, 57344), 255, dtype=torch.uint8, device="cuda:0")]
+    pool = S.slora_pool_create(S.SLORA_F16, 512, 28672, 1, 1, 1, mem, [n, n])
+    desc = dict(cls=1, code=code, n_layers=1, n_heads=4, n_kv_heads=2, head_dim=dim,
+                block_tokens=0 if dim != 256 else 96, max_seqs=4, max_tokens=1000, rot_dim=0)
+    dev = torch.empty(S.slora_kv_device_bytes(pool, **desc), dtype=torch.uint8, device="cuda:0")
+    kv = S.slora_kv_create(pool, dev, dev.numel(), **desc)
+    model, rng, steps, keep = O.KvModel(code, 4, 2, dim, tokens), np.random.default_rng(1), [], []
+    stream = torch.cuda.current_stream()
+
+    def step(seqs, counts, reread):
+        st = S.slora_kv_build_step(kv, seqs, counts, reread)
+        steps.append(st)
+        keep.append(torch.empty(max(16, S.slora_kv_step_get_info(st)["meta_bytes"]), dtype=torch.uint8, device="cuda:0"))
+        S.slora_kv_step_upload(st, keep[-1], keep[-1].numel(), stream)
+        return st
+
+    try:
+        for count, gain in ((500, 1.0), (450, 5.0)):
+            k, v = ((rng.standard_normal((count, 2, dim)) * gain).astype(np.float16) for _ in range(2))
+            S.slora_kv_append(kv, step([1], [count], False), 0, *(torch.from_numpy(x).to("cuda:0") for x in (k, v)),
+                              stream=stream)
+            model.append(1, 0, k, v)
+        made = ([0, 2, 3], [1, 1, 1], [[(3, 901)], [(i, i + 2) for i in range(0, 950, 3)], [(0, 940)]])
+        keep.append(torch.empty(S.slora_kv_take_bytes(kv, *made), dtype=torch.uint8, device="cuda:0"))
+        S.slora_kv_take(kv, *made, keep[-1], keep[-1].numel(), stream)
+        model.take(list(zip(*made)))
+        for i in range(4):
+            n = model.length(i)
+            assert n == S.slora_kv_length(kv, i)
+            x = [torch.zeros((n, 2, dim), dtype=torch.float16, device="cuda:0") for _ in range(2)]
+            S.slora_kv_read(kv, step([i], [n], True), 0, *x, stream)
+            for what in (0, 1):
+                # a rounding of code * range to fp32 and one to fp16; a code's neighbours are further away
+                value = model.values(i, 0, what)
+                assert (np.abs(x[what].cpu().numpy() - value) <= 2.0 ** -10.9 * np.abs(value) + 2.0 ** -25).all()
+    finally:
+        torch.cuda.synchronize()
+        for st in steps:
+            S.slora_kv_step_destroy(st)
+        S.slora_kv_destroy(kv)
+        S.slora_pool_destroy(pool)
+
+
+def test_steps_of_more_metadata_than_a_kernel_uploads():
+    """270000 tokens at once (1.1 MB of metadata, by the copy engine) and in pieces (by a kernel): the same values."""
+    rows, rng = 270000, torch.Generator("cuda").manual_seed(3)
+    k, v = (torch.randn((rows, 1, 64), generator=rng, device="cuda:0").half() for _ in range(2))
+    last = []
+    for pieces in ([rows], [131072, 131072, rows - 262144]):
+        with MoreCase(torch, "f16", 0, 1, 1, 64, 256, rot=0, max_seqs=1, max_tokens=rows) as c:
+            at = 0
+            for n in pieces:
+                st, info, _ = c.step([0], [n])
+                assert (info["meta_bytes"] > 1 << 20) == (n == rows)
+                S.slora_kv_append(c.kv, st, 0, k[at:at + n], v[at:at + n], stream=torch.cuda.current_stream())
+                at += n
+            st, _, _ = c.step([0], [5000], True)
+            x = [torch.zeros((5000, 1, 64), dtype=torch.float16, device="cuda:0") for _ in range(2)]
+            S.slora_kv_read(c.kv, st, 0, *x, torch.cuda.current_stream())
+            last.append(torch.stack(x))
+    assert torch.equal(last[0], last[1])
+    assert (last[0][0] - k[-5000:]).abs().max() < 0.03         # half a code of ranges up to 6
+
+
 def test_another_stream_and_many_at_once():
     """Forks on a stream of their own, ordered by events; a prompt with eight answers beside a shortened sequence."""
     with MoreCase(torch, "f16", 0, 4, 2, 128, 32, n_layers=3, max_seqs=12, max_tokens=300) as c:

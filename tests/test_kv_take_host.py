@@ -48,8 +48,9 @@ def test_binding_checks_its_lists():
         for args in (([1], [0, 0], [None]), ([1], [0], []), ([[1]], [[0]], [None])):
             with pytest.raises(ValueError):
                 S.slora_kv_take(c.kv, *args)
-        with pytest.raises(ValueError):
-            S.slora_kv_take_bytes(c.kv, [1], [0], [[1, 2, 3]])
+        for bad in ([1, 2, 3], [1, 2], [(1, 2, 3)], [(0.0, 1.5)], [[[0, 1]]]):
+            with pytest.raises(ValueError):
+                S.slora_kv_take_bytes(c.kv, [1], [0], [bad])
 
 
 def test_null_arguments():
