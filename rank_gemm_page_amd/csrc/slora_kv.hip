@@ -551,9 +551,11 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
       Pairs<T> xs[N];
       W r[N];
 #pragma unroll
-      for (int n = 0; n < N; ++n) xs[n] = load_pairs(kv, in + min(hh + n, h1 - 1) * kv.dim, a, b);
+      for (int n = 0; n < N; ++n)
+        if (n == 0 || hh + n < h1) xs[n] = load_pairs(kv, in + (hh + n) * kv.dim, a, b);
 #pragma unroll
-      for (int n = 0; n < N; ++n) r[n] = root(head_sum(square_sum<W>(xs[n]), ush), A);
+      for (int n = 0; n < N; ++n)                              // (a head's lanes have the same heads)
+        if (n == 0 || hh + n < h1) r[n] = root(head_sum(square_sum<W>(xs[n]), ush), A);
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         if (hh + n >= h1) break;

@@ -698,7 +698,8 @@ slora_status slora_kv_build_step_window(slora_kv* kv, int32_t n, const int32_t* 
       if (counts[i]) st->n_positions = std::max(st->n_positions, (int32_t)end + shift);
       need += (blocks - s.blocks) * kv->per_block();
       patches += (blocks - s.entered) * kv->per_block();
-      for (int32_t p = start; p < end; ++p) st->row_pos.push_back(p + shift);
+      st->row_pos.resize((size_t)row0 + counts[i]);
+      std::iota(st->row_pos.end() - counts[i], st->row_pos.end(), start + shift);
       for (int32_t b = start / kv->block; counts[i] && b < blocks; ++b)
         st->blocks.push_back({seqs[i], b, std::max(0, start - b * kv->block),
                               (int32_t)std::min<int64_t>(kv->block, end - (int64_t)b * kv->block),

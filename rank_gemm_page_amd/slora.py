@@ -578,7 +578,9 @@ def slora_kv_destroy(kv) -> None:
 
 
 def slora_kv_drop(kv, seq: int) -> None:
-    _check(lib().slora_kv_drop(kv, seq), "slora_kv_drop")
+    status = kv.api.slora_kv_drop(kv, seq)
+    if status:
+        _check(status, "slora_kv_drop")
 
 
 def slora_kv_length(kv, seq: int) -> int:
