@@ -1036,7 +1036,7 @@ slora_status slora_free_pages(slora_pool* p, int32_t cls, int64_t n, const int32
   const int64_t P = p->d.n_pages[cls];
   // validate everything first (including duplicates within ids) so failure changes nothing
   std::vector<int32_t> touched;
-  touched.reserve((size_t)n);
+  touched.reserve((size_t)std::min(n, P));
   slora_status st = SLORA_OK;
   for (int64_t i = 0; i < n; ++i) {
     const int32_t id = ids[i];
