@@ -35,6 +35,19 @@ __global__ __launch_bounds__(kThreads) void kv_rotary_kernel(KvRotary R) {
   const int half = R.half, rows = kThreads / half, pair = threadIdx.x % half, j0 = threadIdx.x / half;
   const int step = rows * kRotSteps;
   const int64_t row0 = (int64_t)blockIdx.x * step * R.bases;
+  if (R.bases == 1) {                                          // a short table: every position's own angle
+    if (j0 < rows)
+#pragma unroll
+      for (int k = 0; k < kRotSteps; ++k) {
+        const int64_t row = row0 + k * rows + j0;
+        double c, s;
+        turn_of((double)(R.first + row), R.turn_hi[pair], R.turn_lo[pair], &c, &s);
+        if (row >= R.n) return;
+        R.out[row * 2 * half + pair] = (float)(c * R.amplitude);
+        R.out[(row * 2 + 1) * half + pair] = (float)(s * R.amplitude);
+      }
+    return;
+  }
   if (j0 < rows) {
     const double hi = R.turn_hi[pair], lo = R.turn_lo[pair];
     for (int b = j0; b < R.bases; b += rows) {
