@@ -192,6 +192,12 @@ namespace {
 // 205 | 214 | 227; 32 requests of 1000 to 3000, 32 heads on 8, of 64 18 | 20 | 21 |
 // 21, of 128 32 | 33 | 35 | 35, of 256 56 | 60 | 64 | 64.
 constexpr int64_t kMinGroups = 8, kWantGroups = 1536;
+// Steps cut for a window: what a round of the chip's places holds, of which a CU has
+// three (heads of 256: two).  us with at most 1536 | 768 | 512 workgroups, window
+// 4096, 8 requests, 32 heads on 8, of 64 14.7 | 12.9 | 13.2, of 128 22.3 | 18.9 | 18.9,
+// of 256 39.3 | 36.6 | 30.2, fp32 of 128 39.7 | 35.9 | 39.2; window 1024, 64 requests,
+// of 128 34.2 | 27.8 | 27.8, of 256 62.7 | 48.7 | 48.7; one request alike.
+constexpr int64_t window_groups(int32_t dim) { return dim == 256 ? 512 : 768; }
 
 // Sequences with at least kPromptMin packed rows (query heads of a kv head times
 // rows), or kFreshMin where nothing was cached before them, take the prompt tiles
@@ -222,7 +228,8 @@ void build_tiles(slora_kv_step* st, int32_t window, int32_t sinks) {
     const int64_t first = std::max<int64_t>(0, s.start + r0 / G - window + 1) / kKvGroup;
     return last - first + std::min<int64_t>(((int64_t)sinks + kKvGroup - 1) / kKvGroup, first);
   };
-  // groups of a workgroup: the fewest for which all row tiles' workgroups are at most kWantGroups
+  // groups of a workgroup: the fewest for which all row tiles' workgroups are at most `want`
+  const int64_t want = window ? window_groups(d.head_dim) : kWantGroups;
   std::vector<int64_t> lens;
   for (const StepSeq& s : st->seqs)
     for (int64_t r0 = 0; !prompt(s) && r0 < (int64_t)s.rows * G; r0 += kKvRows)
@@ -234,7 +241,7 @@ void build_tiles(slora_kv_step* st, int32_t window, int32_t sinks) {
       const int64_t mid = (chunk + high) / 2;
       int64_t wgs = 0;
       for (int64_t n : lens) wgs += (n + mid - 1) / mid;
-      if (wgs * d.n_kv_heads <= kWantGroups) high = mid;
+      if (wgs * d.n_kv_heads <= want) high = mid;
       else chunk = mid + 1;
     }
   }
