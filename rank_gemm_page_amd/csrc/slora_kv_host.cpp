@@ -480,7 +480,8 @@ const char* plan_take(const slora_kv* kv, int32_t n, const int32_t* dst, const i
     if (i == 0 || src[i] != src[i - 1]) {
       ready.resize((size_t)s.entered);
       for (int32_t b = 0; b < s.entered; ++b)
-        ready[b] = *std::min_element(s.stored.begin() + (size_t)b * layers, s.stored.begin() + (size_t)(b + 1) * layers);
+        ready[b] =
+            *std::min_element(s.stored.begin() + (size_t)b * layers, s.stored.begin() + (size_t)(b + 1) * layers);
     }
     kept.clear();
     int64_t end = 0, b = 0;                                    // b: block of the range's first token
@@ -510,7 +511,7 @@ const char* plan_take(const slora_kv* kv, int32_t n, const int32_t* dst, const i
         while (run + 1 < s.runs.size() && s.runs[run + 1].first <= p) ++run;
         const bool last = run + 1 >= s.runs.size();
         const int64_t stop = last ? k.second : std::min<int64_t>(k.second, s.runs[run + 1].first);
-        // a run holds from its first token on; before the first of all there is no shift
+        // a run holds from its first token on, the first from token 0
         const int32_t shift = s.runs.empty() ? 0 : s.runs[run].shift;
         const Seq::Run made = {(int32_t)part.len, (int32_t)(p + shift - part.len)};
         if (part.runs.empty() || part.runs.back().shift != made.shift) part.runs.push_back(made);
@@ -843,8 +844,8 @@ slora_status slora_kv_append_norm(slora_kv* kv, const slora_kv_step* st, int32_t
   if (norm->per_head != 0 && norm->per_head != 1) return fail(SLORA_E_INVAL, f + ": per_head must be 0 or 1");
   if ((reinterpret_cast<uintptr_t>(norm->q_weight) | reinterpret_cast<uintptr_t>(norm->k_weight)) & 15)
     return fail(SLORA_E_INVAL, f + ": the weights must be 16-byte aligned");
-  return append(f, kv, st, layer, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, norm, cos_sin, n_positions,
-                stream);
+  return append(f, kv, st, layer, q, q_stride, q_out, q_out_stride, k, k_stride, v, v_stride, norm, cos_sin,
+                n_positions, stream);
 }
 
 // Frequencies are found in more than 64 bits, as turns a position.

@@ -61,7 +61,8 @@ __global__ __launch_bounds__(kThreads) void kv_rotary_kernel(KvRotary R) {
   if (j0 >= rows) return;
   double cj[kRotSteps], sj[kRotSteps];
 #pragma unroll
-  for (int k = 0; k < kRotSteps; ++k) turn_of((double)(j0 + k * rows), R.turn_hi[pair], R.turn_lo[pair], &cj[k], &sj[k]);
+  for (int k = 0; k < kRotSteps; ++k)
+    turn_of((double)(j0 + k * rows), R.turn_hi[pair], R.turn_lo[pair], &cj[k], &sj[k]);
   for (int b = 0; b < R.bases; ++b) {
     const double2 z = base[b * half + pair];
 #pragma unroll

@@ -65,7 +65,8 @@ __device__ __forceinline__ void take_block(const KvTake& A, uint32_t at, int tid
     const int token = tokens[t], block = (int)((uint32_t)token / (uint32_t)kv.block);
     const int32_t from = row[block];
     const float2 r = *reinterpret_cast<const float2*>(kv.range + 2 * (int64_t)from);
-    return Source{from, token - block * kv.block, __float_as_uint(r.x) & 0x7FFFFFFFu, __float_as_uint(r.y) & 0x7FFFFFFFu};
+    return Source{from, token - block * kv.block, __float_as_uint(r.x) & 0x7FFFFFFFu,
+                  __float_as_uint(r.y) & 0x7FFFFFFFu};
   };
   Source mine = {0, 0, 0, 0};                                  // of token tid
   uint32_t mk = 0, mv = 0, nk = 0, nv = 0;                     // largest, and largest of what the smallest leaves
@@ -106,8 +107,10 @@ __device__ __forceinline__ void take_block(const KvTake& A, uint32_t at, int tid
       const uint64_t p = reinterpret_cast<uint64_t>(base) + vbase + (s >> 5) * 32 * DIM + ((s & 15) >> 2) * 256 +
                          ((s >> 4) & 1) * 4;
       const uint32_t lo = (uint32_t)p, hi = (uint32_t)(p >> 32);
-      const uint32_t ps[4][3] = {{dpp<0x00>(lo), dpp<0x00>(hi), dpp<0x00>(s)}, {dpp<0x55>(lo), dpp<0x55>(hi), dpp<0x55>(s)},
-                                 {dpp<0xAA>(lo), dpp<0xAA>(hi), dpp<0xAA>(s)}, {dpp<0xFF>(lo), dpp<0xFF>(hi), dpp<0xFF>(s)}};
+      const uint32_t ps[4][3] = {{dpp<0x00>(lo), dpp<0x00>(hi), dpp<0x00>(s)},
+                                 {dpp<0x55>(lo), dpp<0x55>(hi), dpp<0x55>(s)},
+                                 {dpp<0xAA>(lo), dpp<0xAA>(hi), dpp<0xAA>(s)},
+                                 {dpp<0xFF>(lo), dpp<0xFF>(hi), dpp<0xFF>(s)}};
       if ((tid & 3) == 0) {
         Quad& q = lds_quad[tid >> 2];
         uint64_t last = 0;
@@ -118,7 +121,8 @@ __device__ __forceinline__ void take_block(const KvTake& A, uint32_t at, int tid
           if (tid + j >= n) {
             rest |= C::kZero << (8 * j);
           } else {
-            if (pj != last) q.word[words++] = reinterpret_cast<const uint8_t*>(pj);   // (tokens ascend: none comes again)
+            // (tokens ascend: no word comes again)
+            if (pj != last) q.word[words++] = reinterpret_cast<const uint8_t*>(pj);
             last = pj;
             const uint32_t w = words - 1, byte = (ps[j][2] & 3) + 4 * (w & 1);
             const uint32_t one = (0x0cu ^ byte) << (8 * j);    // in the place of "none"

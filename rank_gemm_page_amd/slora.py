@@ -630,7 +630,8 @@ def slora_kv_pages(kv, seq: int, layer: int = 0, head: int = 0) -> np.ndarray:
 
 
 def slora_kv_build_step(kv, seqs, counts, reread: bool = False, window: int = 0, sinks: int = 0) -> KvStep:
-    """window, sinks: what its attention will see, where that is a window and the first tokens (the work is cut for it)."""
+    """window, sinks: what its attention will see, where that is a window and the first tokens: the work is cut for
+    it."""
     seqs = np.ascontiguousarray(seqs, dtype=np.int32)
     counts = np.ascontiguousarray(counts, dtype=np.int32)
     if seqs.ndim != 1 or seqs.shape != counts.shape:

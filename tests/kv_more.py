@@ -1,4 +1,5 @@
-"""KvCase with attention over a window and the first tokens, and with sequences made of others' tokens, in all layers."""
+"""KvCase with attention over a window and the first tokens, and with sequences made of others' tokens in all
+layers."""
 import numpy as np
 
 from oracle import kv_oracle as O
