@@ -1080,9 +1080,8 @@ __global__ __launch_bounds__(kThreads) void fetch_words_kernel(uint32_t* to, con
 hipError_t launch_fetch_words(void* to, const void* pinned, int64_t n_words, hipStream_t stream) {
   if (n_words <= 0) return hipSuccess;
   const int64_t blocks = (n_words + 4 * kThreads - 1) / (4 * kThreads);
-  fetch_words_kernel<<<dim3((unsigned)blocks), dim3(kThreads), 0, stream>>>(
-      static_cast<uint32_t*>(to), static_cast<const uint32_t*>(pinned), n_words);
-  return hipGetLastError();
+  void* args[] = {&to, &pinned, &n_words};       // its own status: the last error may be another call's
+  return hipLaunchKernel((const void*)fetch_words_kernel, dim3((unsigned)blocks), dim3(kThreads), args, 0, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -19,10 +19,13 @@ typedef struct { unsigned x, y, z; } dim3_t;
 static int fails_at = -1, last;
 /* The launch after n more ones fails (n < 0: none does). */
 void kv_stub_fail_launch(int n) { fails_at = n; last = 0; }
+/* An error that some earlier call of the program's left. */
+void kv_stub_leave_error(void) { last = 2; }
 hipError_t hipLaunchKernel(const void* f, dim3_t g, dim3_t b, void** a, size_t l, void* s) {
   (void)f; (void)b; (void)a; (void)l; (void)s;
-  if ((fails_at >= 0 && fails_at-- == 0) || !g.x) last = 1;
-  return last;
+  const int e = (fails_at >= 0 && fails_at-- == 0) || !g.x;
+  if (e) last = e;
+  return e;
 }
 /* What kernel<<<...>>> passes through. */
 static struct { dim3_t g, b; size_t l; void* s; } call;

@@ -153,6 +153,19 @@ def test_a_failed_launch_changes_nothing():
 
 
 @stubbed
+def test_errors_of_others_are_not_taken_for_its_own():
+    """What an earlier HIP call of the program's failed with is still to be asked for when a launch succeeds."""
+    stub = ctypes.CDLL(STUB)
+    with Cache(n_pages=100, max_seqs=4, max_tokens=300) as c:
+        life = Life(c, 4, 32)
+        stub.kv_stub_leave_error()
+        life.grow([0], [100])
+        life.take([(1, 0, [(3, 90)])])
+        life.check(100)
+        stub.kv_stub_fail_launch(-1)
+
+
+@stubbed
 def test_captured_streams_shared_blocks_and_stale_steps():
     with Cache(n_pages=100, max_seqs=4, max_tokens=300) as c:
         life = Life(c, 4, 32)
