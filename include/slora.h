@@ -755,7 +755,8 @@ slora_status slora_kv_attend_sinks(slora_kv* kv, const slora_kv_step* step, int3
  * at least slora_kv_take_bytes, 16-byte aligned, kept untouched until the launches
  * are done) and launches on `stream`, without waiting; ordered as uploads and
  * launches are, and launches that still read freed pages must be ordered before
- * whatever the caller lets write them next.  Refused while `stream` is captured. */
+ * whatever the caller lets write them next.  Refused while `stream` is captured, also
+ * where the call would launch nothing. */
 slora_status slora_kv_take(slora_kv* kv, int32_t n, const int32_t* dst, const int32_t* src, const int32_t* n_ranges,
                            const int64_t* ranges, void* dev_meta, size_t dev_meta_bytes, void* stream);
 /* Bytes of device metadata that such a call needs as things stand; 0 on a bad

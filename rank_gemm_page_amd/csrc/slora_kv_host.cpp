@@ -953,10 +953,15 @@ slora_status slora_kv_take(slora_kv* kv, int32_t n, const int32_t* dst, const in
       if (dev_meta_bytes < plan.bytes()) return fail(SLORA_E_NOMEM, f + ": dev_meta smaller than slora_kv_take_bytes");
       slora_status ok = pool_device_current(kv->pool);
       if (ok != SLORA_OK) return ok;
+    }
+    if (n > 0) {
+      // Also where nothing is launched: launches that the graph holds already would
+      // read freed pages.  (Such a call needs no device, so asking for one may fail.)
       hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
       const hipError_t e = hipStreamIsCapturing(hs, &capture);
-      if (e != hipSuccess) return fail(SLORA_E_HIP, f + ": hipStreamIsCapturing: " + hipGetErrorString(e));
-      if (capture != hipStreamCaptureStatusNone)
+      if (e != hipSuccess && works) return fail(SLORA_E_HIP, f + ": hipStreamIsCapturing: " + hipGetErrorString(e));
+      if (e != hipSuccess) (void)hipGetLastError();              // not for a later call to find
+      if (e == hipSuccess && capture != hipStreamCaptureStatusNone)
         return fail(SLORA_E_INVAL, f + ": the stream is captured, which this call cannot be");
     }
     // everything that can run out of host memory
