@@ -640,8 +640,8 @@ slora_status slora_kv_append(slora_kv* kv, const slora_kv_step* step, int32_t la
  *
  *     x_i' = x_i / sqrt(mean_j x_j^2 + eps) * w_i
  *
- * k is normed in 64 bits (as it is rotated there), q in fp32 (in fp32 pools in 64
- * bits, and rounded to fp32 before the rotation).  q_weight and k_weight are
+ * k is normed in 64 bits (as it is rotated there), q in fp32 (in fp32 pools normed and
+ * rotated in 64 bits and rounded once).  q_weight and k_weight are
  * device memory of the pool dtype, 16-byte aligned: head_dim elements for all
  * heads, or, with per_head, n_heads (n_kv_heads) times head_dim; NULL: ones.
  * v is stored as it is.  eps is at least 2^-126 and finite. */

@@ -75,7 +75,8 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t x, int lane) {
 // a wave takes one token, in all its lanes.  256 decode tokens of 32 heads take 14.4 us
 // instead of the 10.8 without norms; 32 prompts of 64 to 512 tokens 118 us (3.3
 // TB/s) instead of 85: keys take 122 registers where values take 80, so that 3.4
-// waves a SIMD run, which issue vector instructions in 57 % of the cycles.
+// waves a SIMD run, which issue vector instructions in 57 % of the cycles.  fp32, 32
+// prompts of 9585 tokens together, 32 heads on 8: 90 us (4.6 TB/s) instead of 85.
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
@@ -113,8 +114,9 @@ __device__ __forceinline__ Pairs<T> load_weights(const KvAppend& A, const void* 
   for (int j = 0; j < 8; ++j) r.a[j] = r.b[j] = (T)1.f;
   return r;
 }
-// q's norm: in fp32, whose squares and sums hold those of fp16 numbers; fp32 ones
-// may lie anywhere and take 64 bits.
+// q's norm and its rotation: in fp32, whose squares and sums hold those of fp16
+// numbers and whose roundings are small beside the output's; fp32 ones may lie
+// anywhere and take 64 bits, which are rounded once.
 template <typename T> struct Norm { typedef float type; };
 template <> struct Norm<float> { typedef double type; };
 template <typename W, typename T>
@@ -566,8 +568,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppend A) {
         if (A.w_stride) w = load_weights<T>(A, A.q_weight, hh + n, a, b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float xa = (float)((W)x.a[j] * r[n] * (W)w.a[j]), xb = (float)((W)x.b[j] * r[n] * (W)w.b[j]);
-          float ra = xa, rb = xb;
+          const W xa = (W)x.a[j] * r[n] * (W)w.a[j], xb = (W)x.b[j] * r[n] * (W)w.b[j];
+          W ra = xa, rb = xb;
           if (turns) turned(xa, xb, t.c[j], t.s[j], &ra, &rb);
           x.a[j] = (T)ra;
           x.b[j] = (T)rb;
