@@ -578,7 +578,7 @@ def slora_kv_destroy(kv) -> None:
 
 
 def slora_kv_drop(kv, seq: int) -> None:
-    status = kv.api.slora_kv_drop(kv, seq)
+    status = lib().slora_kv_drop(kv, seq)
     if status:
         _check(status, "slora_kv_drop")
 
