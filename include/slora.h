@@ -675,7 +675,7 @@ slora_status slora_kv_append_norm(slora_kv* kv, const slora_kv_step* step, int32
  *
  * base > 1, factor >= 1, trained >= 1, 0 < low < high (the last three only where
  * they are used) and amplitude are finite.  cos_sin is device memory, fp32 [n][rot_dim],
- * 16-byte aligned.  One launch on `stream`; refused where rot_dim is 0. */
+ * 16-byte aligned (NULL where n is 0).  One launch on `stream`; refused where rot_dim is 0. */
 typedef enum {
   SLORA_KV_ROT_NONE = 0,
   SLORA_KV_ROT_LINEAR = 1,

@@ -852,7 +852,7 @@ slora_status slora_kv_append_norm(slora_kv* kv, const slora_kv_step* st, int32_t
 slora_status slora_kv_rotary_table(slora_kv* kv, const slora_kv_rotary* r, int64_t first, int64_t n, float* cos_sin,
                                    void* stream) {
   const std::string f = "slora_kv_rotary_table";
-  if (!kv || !r || !cos_sin) return fail(SLORA_E_INVAL, f + ": NULL argument");
+  if (!kv || !r || (!cos_sin && n != 0)) return fail(SLORA_E_INVAL, f + ": NULL argument");
   const int32_t rot = kv->d.rot_dim;
   if (!rot) return fail(SLORA_E_INVAL, f + ": the cache rotates nothing (rot_dim 0)");
   if (reinterpret_cast<uintptr_t>(cos_sin) & 15) return fail(SLORA_E_INVAL, f + ": cos_sin must be 16-byte aligned");

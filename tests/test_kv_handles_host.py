@@ -14,3 +14,14 @@ def test_sequences_are_dropped_by_any_handle():
         c.step([0], [40])
         S.slora_kv_drop(ctypes.c_void_p(c.kv.value), 0)
         assert S.slora_kv_length(c.kv, 0) == 0
+
+
+def test_a_table_of_no_positions_has_no_address():
+    """An empty tensor's address is NULL; where there are positions, NULL is refused."""
+    table = dict(first=5, scaling="linear", factor=2.0)
+    with Cache() as c:
+        S.slora_kv_rotary_table(c.kv, 0, n_positions=0, **table)
+        refused(INVAL, S.slora_kv_rotary_table, c.kv, 0, n_positions=1, **table)
+        refused(INVAL, S.slora_kv_rotary_table, c.kv, 8, n_positions=0, **table)
+        refused(INVAL, S.slora_kv_rotary_table, c.kv, 0, n_positions=0, first=-1)
+        refused(INVAL, S.slora_kv_rotary_table, c.kv, 0, n_positions=0, base=1.0)
