@@ -27,6 +27,7 @@
 
 #include "slora.h"
 #include "slora_internal.h"
+#include "slora_kv.h"
 
 using namespace slora;
 
@@ -1351,13 +1352,12 @@ slora_status slora_segments_upload(slora_segments* s, void* dev_meta, size_t dev
   if (dev_meta_bytes < meta_bytes_of(s)) return fail(SLORA_E_NOMEM, "slora_segments_upload: dev_meta smaller than meta_bytes");
   slora_pool* p = s->pool;
   if (bytes > 0) {
-    hipStream_t st_ = static_cast<hipStream_t>(stream);
-    slora_status st = pool_upload(p, dev_meta, s->blob.data(), bytes, st_);
-    if (st != SLORA_OK) return st;
     // error word and v pairs start at zero; fused launches count epochs from 1
-    hipError_t e = launch_zero_words(static_cast<int32_t*>(dev_meta) + s->error_off_words,
-                                     (int64_t)(meta_bytes_of(s) / 4) - s->error_off_words, st_);
-    if (e != hipSuccess) return hip_fail(e, "zeroing the fused-launch area");
+    UploadWith with;
+    with.zero = static_cast<int32_t*>(dev_meta) + s->error_off_words;
+    with.zero_words = (int64_t)(meta_bytes_of(s) / 4) - s->error_off_words;
+    slora_status st = pool_upload(p, dev_meta, s->blob.data(), bytes, static_cast<hipStream_t>(stream), with);
+    if (st != SLORA_OK) return st;
   }
   s->dev_meta = static_cast<const int32_t*>(dev_meta);
   s->epoch = 0;
@@ -1424,7 +1424,8 @@ void slora::pool_return_pages(slora_pool* p, int32_t cls, int64_t n, const int32
   }
 }
 
-slora_status slora::pool_upload(slora_pool* p, void* dst, const void* src, size_t bytes, hipStream_t stream) {
+slora_status slora::pool_upload(slora_pool* p, void* dst, const void* src, size_t bytes, hipStream_t stream,
+                                const UploadWith& with) {
   slora_status st = set_device(p);
   if (st != SLORA_OK) return st;
   const int slot = p->meta_slot;
@@ -1447,17 +1448,28 @@ slora_status slora::pool_upload(slora_pool* p, void* dst, const void* src, size_
   }
   std::memcpy(p->h_meta[slot], src, bytes);
   // A copy engine between two kernels leaves the GPU idle meanwhile; a kernel that
-  // reads the slot does not: an upload of 10 KB (which the runtime copies by a
-  // kernel itself) takes 9 us of a stream either way, of 86 KB 22.5 and 10.9, of 278
-  // KB 26 and 15; 1.1 MB takes 41 by the engine.
-  if (bytes <= kFetchBytes && bytes % 4 == 0)
-    e = launch_fetch_words(dst, p->h_meta[slot], (int64_t)(bytes / 4), stream);
+  // reads the slot does not, and does at once what would follow the copy.  A step's
+  // upload on an idle GPU, us between events of its stream by the engine and a second
+  // kernel | by one kernel: 1.7 KB (which the runtime copies by a kernel itself) 12.6 |
+  // 11.2, 46 KB 22.1 | 11.0, 184 KB 25.4 | 13.9, 576 KB 32.3 | 22.9; 1.9 MB takes 105
+  // by the engine.  Beside products of 8192^3 on another stream (825 us each), which
+  // leave a kernel no place before they end, either takes 810 to 825, and the copy and
+  // the rest in a kernel each 1630.
+  const bool fetch = bytes <= kFetchBytes && bytes % 4 == 0;
+  if (fetch)
+    e = launch_fetch_words(dst, p->h_meta[slot], (int64_t)(bytes / 4), with, stream);
   else
     e = hipMemcpyAsync(dst, p->h_meta[slot], bytes, hipMemcpyHostToDevice, stream);
   if (e != hipSuccess) return hip_fail(e, "the metadata's copy");
   e = hipEventRecord(p->meta_done[slot], stream);
   if (e != hipSuccess) return hip_fail(e, "hipEventRecord(metadata)");
   p->meta_slot ^= 1;
+  if (fetch) return SLORA_OK;
+  e = launch_zero_words(with.zero, with.zero_words, stream);
+  if (e == hipSuccess)
+    e = launch_kv_patch(with.table, reinterpret_cast<const KvPatch*>(static_cast<char*>(dst) + with.patches_off),
+                        with.n_patches, stream);
+  if (e != hipSuccess) return hip_fail(e, "what goes with the metadata");
   return SLORA_OK;
 }
 

@@ -22,9 +22,19 @@ struct PoolInfo {
   char* base[2];
 };
 bool pool_info(const slora_pool* pool, PoolInfo* info);
-// Queue a copy of host bytes to dst on `stream` through the pool's pinned
-// metadata slots (src may be reused at once).
-slora_status pool_upload(slora_pool* pool, void* dst, const void* src, size_t bytes, hipStream_t stream);
+// What an upload does beside its copy: words that it clears, and page table
+// entries (KvPatch records from byte patches_off on) that it enters in the table.
+struct UploadWith {
+  void* zero = nullptr;         // 16-byte aligned
+  int64_t zero_words = 0;
+  int32_t* table = nullptr;
+  size_t patches_off = 0;       // a multiple of 16
+  int32_t n_patches = 0;
+};
+// Queue a copy of host bytes to dst (16-byte aligned) on `stream` through the
+// pool's pinned metadata slots (src may be reused at once).
+slora_status pool_upload(slora_pool* pool, void* dst, const void* src, size_t bytes, hipStream_t stream,
+                         const UploadWith& with = {});
 // KV pages that a call took and holds: back to the head of the free list, as if it
 // had never taken them, or to its tail.  Neither can fail.
 void pool_untake_pages(slora_pool* pool, int32_t cls, int64_t n, const int32_t* ids);
@@ -204,7 +214,9 @@ hipError_t launch_forward(const ForwardLaunch& F, hipStream_t stream, hipEvent_t
 
 // Zero n_words 32-bit words at p (a fill kernel; no memset node in the stream).
 hipError_t launch_zero_words(void* p, int64_t n_words, hipStream_t stream);
-hipError_t launch_fetch_words(void* to, const void* pinned, int64_t n_words, hipStream_t stream);
+// Copy n_words words from pinned host memory, and what the upload does beside.
+hipError_t launch_fetch_words(void* to, const void* pinned, int64_t n_words, const UploadWith& with,
+                              hipStream_t stream);
 
 // Adapter images staged on the device for one scatter launch.  Image i sits
 // at stage + img_off[i]: n_proj x rank[i] A^T rows of a_row_bytes, then as many

@@ -1067,20 +1067,38 @@ hipError_t launch_zero_words(void* p, int64_t n_words, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Pinned host memory read by a kernel: 16 bytes a thread, the last ones word by word.
-__global__ __launch_bounds__(kThreads) void fetch_words_kernel(uint32_t* to, const uint32_t* from, int64_t n) {
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (i + 4 <= n) {
-    *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(from + i);
+// Pinned host memory read by a kernel: 16 bytes a thread, the last ones word by
+// word; a page table entry is such 16 bytes.  Threads behind the copy's clear words.
+struct Fetch {
+  uint32_t* to;
+  const uint32_t* from;
+  uint32_t* zero;
+  int32_t* table;
+  int64_t n, zero_words, patch0, patch1;         // the entries are words patch0 .. patch1
+};
+__global__ __launch_bounds__(kThreads) void fetch_words_kernel(Fetch F) {
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4, z = i - (F.n + 3) / 4 * 4;
+  if (i + 4 <= F.n) {
+    const uint4 w = *reinterpret_cast<const uint4*>(F.from + i);
+    *reinterpret_cast<uint4*>(F.to + i) = w;
+    if (i >= F.patch0 && i < F.patch1) F.table[((int64_t)w.y << 32) | w.x] = (int32_t)w.z;
+  } else if (z < 0) {
+    for (int64_t j = i; j < F.n; ++j) F.to[j] = F.from[j];
+  } else if (z + 4 <= F.zero_words) {
+    *reinterpret_cast<uint4*>(F.zero + z) = make_uint4(0, 0, 0, 0);
   } else {
-    for (int64_t j = i; j < n; ++j) to[j] = from[j];
+    for (int64_t j = z; j < F.zero_words; ++j) F.zero[j] = 0u;
   }
 }
 
-hipError_t launch_fetch_words(void* to, const void* pinned, int64_t n_words, hipStream_t stream) {
-  if (n_words <= 0) return hipSuccess;
-  const int64_t blocks = (n_words + 4 * kThreads - 1) / (4 * kThreads);
-  void* args[] = {&to, &pinned, &n_words};       // its own status: the last error may be another call's
+hipError_t launch_fetch_words(void* to, const void* pinned, int64_t n_words, const UploadWith& with,
+                              hipStream_t stream) {
+  const int64_t blocks = ((n_words + 3) / 4 + (with.zero_words + 3) / 4 + kThreads - 1) / kThreads;
+  if (blocks <= 0) return hipSuccess;
+  Fetch F{static_cast<uint32_t*>(to), static_cast<const uint32_t*>(pinned), static_cast<uint32_t*>(with.zero),
+          with.table, n_words, with.zero_words, (int64_t)(with.patches_off / 4), 0};
+  F.patch1 = F.patch0 + 4 * (int64_t)with.n_patches;
+  void* args[] = {&F};                           // its own status: the last error may be another call's
   return hipLaunchKernel((const void*)fetch_words_kernel, dim3((unsigned)blocks), dim3(kThreads), args, 0, stream);
 }
 

@@ -810,12 +810,11 @@ slora_status slora_kv_step_upload(slora_kv_step* st, void* dev_meta, size_t dev_
     put(st->tiles_off() + st->tiles.size() * sizeof(KvTile), st->combine.data(), st->combine.size() * sizeof(KvTile));
     put(st->patches_off(), st->patches.data(), st->patches.size() * sizeof(KvPatch));
     put(st->row_pos_off(), st->row_pos.data(), st->row_pos.size() * sizeof(int32_t));
-    hipStream_t hs = static_cast<hipStream_t>(stream);
-    ok = pool_upload(kv->pool, dev_meta, image.data(), image.size(), hs);
-    if (ok != SLORA_OK) return ok;
-    const char* dev = static_cast<const char*>(dev_meta);
-    ok = launched(f, launch_kv_patch(kv->table(), reinterpret_cast<const KvPatch*>(dev + st->patches_off()),
-                                     (int32_t)st->patches.size(), hs));
+    UploadWith with;
+    with.table = kv->table();
+    with.patches_off = st->patches_off();
+    with.n_patches = (int32_t)st->patches.size();
+    ok = pool_upload(kv->pool, dev_meta, image.data(), image.size(), static_cast<hipStream_t>(stream), with);
     if (ok != SLORA_OK) return ok;
   }
   for (size_t i = 0; i < st->seqs.size(); ++i) {
