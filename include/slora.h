@@ -501,7 +501,8 @@ const char* slora_last_error(void);
  * head then reads as NaN: it is never lost silently.
  *
  * Position p of a sequence is its p-th token (0, 1, ...), until slora_kv_take
- * leaves tokens out: the others keep theirs.  Rotation by positions: for the pairs (a_i, b_i), i = 0 .. rot_dim/2 - 1, of a head,
+ * leaves tokens out: the others keep theirs.  Rotation by positions: for the pairs
+ * (a_i, b_i), i = 0 .. rot_dim/2 - 1, of a head,
  *
  *     a_i' = a_i cos(p, i) - b_i sin(p, i)     b_i' = b_i cos(p, i) + a_i sin(p, i)
  *
@@ -510,7 +511,10 @@ const char* slora_last_error(void);
  * rotated in 64 bits before they are coded, q in fp32 (a product and the sum
  * rounded once each) and rounded to the pool dtype.  cos_sin is the caller's
  * table, device fp32 [n_positions][rot_dim]: a position's rot_dim/2 cosines, then
- * its rot_dim/2 sines.
+ * its rot_dim/2 sines.  It begins at position 0, so that an append needs 4 *
+ * rot_dim bytes for every position up to the last of its own, also in a sequence
+ * that is shortened again and again (slora_kv_position counts on): 512 MB for a
+ * million positions of 128.
  *
  * One step of a server: slora_kv_build_step names the sequences of the batch
  * and how many tokens each one gains, slora_kv_step_upload brings the step to
@@ -658,7 +662,10 @@ slora_status slora_kv_append_norm(slora_kv* kv, const slora_kv_step* step, int32
 
 /* The table of cosines and sines that append takes, for positions first ..
  * first + n - 1 (up to 2^30): row p - first holds amplitude * cos(p f_i), i = 0 ..
- * rot_dim/2 - 1, then amplitude * sin(p f_i), each from 64 bits and rounded once.
+ * rot_dim/2 - 1, then amplitude * sin(p f_i), each found in 64 bits and rounded
+ * once: beside that rounding an entry is off by at most |amplitude| (2^-49 + p 2^-59),
+ * where 2^-49 is the sine's and p 2^-59 the frequency's, which is found in
+ * long double (64 bits of it; BANDS: times high / (high - low)).
  * With t_i = base^(-2i / rot_dim) the frequencies are
  *
  *   SLORA_KV_ROT_NONE    f_i = t_i
@@ -675,7 +682,7 @@ slora_status slora_kv_append_norm(slora_kv* kv, const slora_kv_step* step, int32
  *
  * base > 1, factor >= 1, trained >= 1, 0 < low < high (the last three only where
  * they are used) and amplitude are finite.  cos_sin is device memory, fp32 [n][rot_dim],
- * 16-byte aligned (NULL where n is 0).  One launch on `stream`; refused where rot_dim is 0. */
+ * 16-byte aligned (it may be NULL where n is 0).  One launch on `stream`; refused where rot_dim is 0. */
 typedef enum {
   SLORA_KV_ROT_NONE = 0,
   SLORA_KV_ROT_LINEAR = 1,

@@ -180,8 +180,8 @@ class KvModel:
 
     def attend(self, seq, layer, q, start, scale, window=0, length=None, sinks=0):
         """Rows q [n, n_heads, dim] (rotated) at positions start, start + 1, ... over the first `length` tokens (all by
-        default), each over the window and the first `sinks` tokens.  Returns the output and, per output, sum_j w_j |v_j|, the largest sum of |scale q k| over the seen
-        keys and sum_j |v_j| / sum_j exp(s_j - max s) for error bounds."""
+        default), each over the window and the first `sinks` tokens.  Returns the output and, per output,
+        sum_j w_j |v_j|, the largest sum of |scale q k| over the seen keys and sum_j |v_j| / sum_j exp(s_j - max s) for error bounds."""
         k, v = (self.values(seq, layer, w, 0, length) for w in (0, 1))
         q = np.asarray(q, np.float64)
         n, g = len(q), self.n_heads // self.n_kv

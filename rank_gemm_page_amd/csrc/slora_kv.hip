@@ -671,10 +671,15 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, int splits, uint32_t*
 // Groups of 32 keys that a tile sees, from key lo to key last: with sinks, the
 // groups of the first tokens and then the window's are counted as one run, of
 // which the first `sinks` lie at the sequence's start, so that splits over waves and
-// workgroups may begin on either side of the jump.  It costs 6 registers in the row
-// tiles and as many in the prompt tiles, in instances of their own.  64 requests,
-// window 1024, 32 heads on 8: 27 us, 5.0 TB/s of codes; 2048 tokens after 6001, window
-// 2048, 64 heads on 8: 224 us, 631 TFLOP/s.
+// workgroups may begin on either side of the jump.  In instances of their own: 0 to 7
+// vector registers more in the row tiles (fp32 e4m3 of 128 164 to 171, three waves a
+// SIMD to two; all e4m3 ones spill 5 to 9 scalar ones), in the prompt tiles 5 to 6 of
+// 195 for heads of 128 and 16 of 127 for heads of 64 (four waves a SIMD to three).  us
+// with first tokens | with as many more keys in the window: 64 requests, window 1024
+// and 4, 32 heads on 8, heads of 64 17 | 16, of 128 27 | 26 (5.0 TB/s of codes), of 256
+// (16 on 4) 29 | 28, fp32 e4m3 of 128 66 | 63; 2048 tokens after 6001, window 2048 and
+// 64, 64 heads on 8, heads of 64 145 | 128, of 128 221 | 217 (640 TFLOP/s), of 256 (32
+// on 4) 403 | 408.
 template <bool SINKS> struct Seen;
 template <> struct Seen<false> {
   static constexpr int sinks = 0;

@@ -192,8 +192,9 @@ namespace {
 // 205 | 214 | 227; 32 requests of 1000 to 3000, 32 heads on 8, of 64 18 | 20 | 21 |
 // 21, of 128 32 | 33 | 35 | 35, of 256 56 | 60 | 64 | 64.
 constexpr int64_t kMinGroups = 8, kWantGroups = 1536;
-// Steps cut for a window: what a round of the chip's places holds, of which a CU has
-// three (heads of 256: two).  us with at most 1536 | 768 | 512 workgroups, window
+// Steps cut for a window: three workgroups a CU (heads of 256: two), a round of the
+// chip's places for heads of 128.  (Heads of 64 have four places a CU, fp32 e4m3 ones of
+// 128 with first tokens two; the rule leaves that out.)  us with at most 1536 | 768 | 512 workgroups, window
 // 4096, 8 requests, 32 heads on 8, of 64 14.7 | 12.9 | 13.2, of 128 22.3 | 18.9 | 18.9,
 // of 256 39.3 | 36.6 | 30.2, fp32 of 128 39.7 | 35.9 | 39.2; window 1024, 64 requests,
 // of 128 34.2 | 27.8 | 27.8, of 256 62.7 | 48.7 | 48.7; one request alike.

@@ -20,8 +20,9 @@ constexpr int kRotBases = 16;     // bases of a workgroup, at most
 
 // Angles are held in turns: p * (hi + lo) of a position p below 2^31 leaves its
 // whole turns exactly (the product's rounding error comes back from the fma, so
-// nothing else may be fused with the product), and far positions are as good as
-// near ones.
+// nothing else may be fused with the product).  What far positions lose is the
+// frequency's own error times p, 2^-59 p at most: frequencies are found in 64 bits of
+// mantissa (about 6 units of 2^-64 of the exponentials, 6 of what follows them).
 __device__ __forceinline__ void turn_of(double p, double hi, double lo, double* c, double* s) {
 #pragma clang fp contract(off)
   const double whole = p * hi, rest = __builtin_fma(p, hi, -whole) + p * lo;
